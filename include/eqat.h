@@ -315,6 +315,119 @@ eqat_status eqat_fq_linear_fwd_noalloc(const void *X, const void *W, int dt, con
                                        const float *z, void *Y, int64_t M, int64_t N, int64_t K,
                                        int bits, int group, eqat_stream_t stream);
 
+/* ------------------------------------------------------------------------------
+ * Rows of logits
+ *
+ * x is [T, V], bf16 or fp32, with a row stride of ld >= V elements: a padded
+ * vocabulary is passed as a view, and the columns past V are neither read nor
+ * written.  x is 16-byte aligned; the other arrays need their element's alignment
+ * only (a shifted view of the labels is fine).  temperature is within 1e-6 .. 1e6 and
+ * divides the logits; an entry of -inf is masked: it has no probability and is never
+ * an alternative.  V < 2^31.
+ *
+ * eqat_token_logprobs: with lse the log of sum exp(x / temperature) over a row,
+ *   logprob[t] = x[t, targets[t]] / temperature - lse      0 where targets[t] < 0,
+ *                                                          NaN where targets[t] >= V
+ *   entropy[t] = -sum p ln p, p = exp(x / temperature - lse)
+ *   top_ids, top_logprobs [T, top_k]: the top_k largest entries in falling order,
+ *     the lowest index first among equal ones (-0 equals 0); where fewer entries are
+ *     not masked, the rest have id -1 and -inf.
+ * top_k within 0..EQAT_TOP_MAX (0: both arrays are ignored).  A row whose entries are
+ * all masked gives -inf (0 for a negative target), entropy 0 and no alternatives.  A
+ * row with NaN or +inf gives NaN (0 for a negative target) and ids of -1. */
+#define EQAT_TOP_MAX 128
+eqat_status eqat_token_logprobs(const void *x, int dt, int64_t ld, int64_t T, int64_t V, const int64_t *targets,
+                                double temperature, int top_k, float *logprob, float *entropy, int64_t *top_ids,
+                                float *top_logprobs, eqat_stream_t stream);
+
+/* eqat_distill_topk: the loss of a student's logits x against a teacher's k
+ * alternatives per row (1 <= k <= EQAT_TOP_MAX), and its gradient.  ids [T, k] are the
+ * alternatives (negative: an empty slot) and tlp [T, k] their log probabilities, as
+ * eqat_token_logprobs gives them.  With p = softmax(x / temperature):
+ *   flags 0: q = the teacher's masses renormalised over the slots (tlp may then be
+ *     any logits),  L = sum_i q_i (ln q_i - ln p_i);
+ *   EQAT_DISTILL_TAIL: q_i = exp(tlp_i), and what the teacher has outside the slots,
+ *     q_r = max(0, 1 - sum q_i), is compared with the student's mass outside them:
+ *     L = sum_i q_i (ln q_i - ln p_i) + q_r (ln q_r - ln p_r).  The last term is left
+ *     out where q_r = 0 or every entry outside the slots is masked.
+ *   loss[t] = weight[t] L                                   [T] fp32   (nullable)
+ *   dx = weight[t] dL/dx, dtype dt, row stride ld           [T, V]     (nullable)
+ * weight (nullable: all 1) is the token's weight, or the gradient that arrives at its
+ * loss.  dx may be x itself.  A row of weight 0 is not read: loss 0, dx 0.  The same
+ * holds, whatever its weight, for a row whose teacher has no mass (renormalised form)
+ * and for one whose entries are all masked.  A masked entry under a slot with mass
+ * gives a loss of +inf and a finite gradient.  An id given twice counts with its
+ * slots' masses together.  An id >= V, NaN or +inf in the row, or NaN or +inf in
+ * tlp, makes the row's loss and gradient NaN.  V <= EQAT_DISTILL_MAX_V. */
+#define EQAT_DISTILL_TAIL 1u
+#define EQAT_DISTILL_MAX_V 1048576
+eqat_status eqat_distill_topk(const void *x, int dt, int64_t ld, int64_t T, int64_t V, const int64_t *ids,
+                              const float *tlp, int k, double temperature, uint32_t flags, const float *weight,
+                              float *loss, void *dx, eqat_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * Microscaled 4-bit floats
+ *
+ * Blocks of consecutive in-features of a row share an 8-bit scale; a value is an e2m1
+ * code c: (-1)^(c >> 3) {0, .5, 1, 1.5, 2, 3, 4, 6}[c & 7].
+ *   EQAT_FP4_MX: blocks of 32; scale byte b = e + 127 stands for 2^e (e8m0), with
+ *     e = max(floor(log2 amax) - 2, -127); code = RNE(x 2^-e), at most 6.
+ *   EQAT_FP4_NV: blocks of 16; scale byte = e4m3 s, over a scale g > 0 of the tensor
+ *     (one fp32 value in device memory, NULL: 1):  x' = x (1/g),
+ *     s = RNE_e4m3(min(amax' / 6, 448)),  code = RNE(x' / s) (magnitude 0 where s = 0), and the
+ *     value is code * s * g.  All of it in IEEE fp32; with g a power of two (which
+ *     eqat_fp4_tensor_scale gives) every decision is that of exact arithmetic.  1/g
+ *     and x' must be finite.
+ * RNE: to nearest, ties to the even code; a zero keeps the sign of x.  A block with a NaN or an infinity gets a
+ * NaN scale (0xFF; 0x7F) and zero codes: it reads back, and multiplies, as NaN.
+ *
+ * codes [N, K/2]: the code of column k in bits 4 (k % 2).  scales: tiles of 128 rows
+ * by 4 blocks, 512 bytes each, [ceil(N/128)][ceil(G/4)][512] with G = K / block; the
+ * scale of row r, block j is byte 16 (r % 32) + 4 ((r % 128) / 32) + j % 4 of its tile
+ * (the order in which the tensor cores take them).  Packing writes the rows past N and
+ * the blocks past G of the last tiles as 0.  K % 32 == 0; x, codes, scales and values
+ * 16-byte aligned; M, N, K < 2^31. */
+typedef enum { EQAT_FP4_MX = 0, EQAT_FP4_NV = 1 } eqat_fp4_format;
+
+/* Bytes of the scale tiles of an [N, K] matrix (0 for bad arguments). */
+size_t eqat_fp4_scale_bytes(int64_t N, int64_t K, int fmt);
+
+/* g: the smallest power of two within 2^-100 .. 2^100 with max|x| <= 6 * 448 * g over
+ * the n finite values of x (n % 32 == 0); one fp32 value. */
+eqat_status eqat_fp4_tensor_scale(const void *x, int dt, int64_t n, float *g, eqat_stream_t stream);
+
+/* x [N, K] (dt bf16 or fp32) -> codes, scales. */
+eqat_status eqat_pack_fp4(const void *x, int dt, int64_t N, int64_t K, int fmt, const float *g, uint8_t *codes,
+                          uint8_t *scales, eqat_stream_t stream);
+
+/* The values that packing would store, x_hat [N, K] of dtype dt (exact in bf16 when g
+ * is a power of two; otherwise rounded to nearest even). */
+eqat_status eqat_fake_quant_fp4(const void *x, int dt, int64_t N, int64_t K, int fmt, const float *g, void *x_hat,
+                                eqat_stream_t stream);
+
+/* The values of packed codes, [N, K] of dtype dt. */
+eqat_status eqat_dequant_fp4(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K, int fmt,
+                             const float *g, void *values, int dt, eqat_stream_t stream);
+
+/* Bytes of workspace of eqat_fp4_linear_fwd (backward == 0: X's codes and scales) or
+ * eqat_fp4_linear_bwd (the bf16 values of W and X); 0 for bad arguments. */
+size_t eqat_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int backward);
+
+/* Y = X_hat W_hat^T with both operands in 4 bits: X [M, K] is packed in the call (with
+ * the tensor scale gx of its own), W comes packed (tensor scale gw).  X and Y bf16.
+ * Products of codes and scales are exact, sums are fp32 on the tensor cores, and the
+ * tensor scales multiply the sum before the one rounding to bf16.  N % 8 == 0. */
+eqat_status eqat_fp4_linear_fwd(const void *X, const uint8_t *codes, const uint8_t *scales, int fmt,
+                                const float *gx, const float *gw, void *Y, int64_t M, int64_t N, int64_t K,
+                                void *ws, size_t ws_bytes, eqat_stream_t stream);
+
+/* The straight-through backward of eqat_fp4_linear_fwd (packing has an identity
+ * gradient):  dX = dY W_hat  [M, K],  dW = dY^T X_hat  [N, K], both bf16 and nullable,
+ * with the bf16 values of the packed operands. */
+eqat_status eqat_fp4_linear_bwd(const void *X, const uint8_t *codes, const uint8_t *scales, int fmt,
+                                const float *gx, const float *gw, const void *dY, void *dX, void *dW, int64_t M,
+                                int64_t N, int64_t K, void *ws, size_t ws_bytes, eqat_stream_t stream);
+
 /* Synchronises `stream`, then reads and clears the device error word of the
  * current device.  Returns EQAT_OK, EQAT_ERR_TIMEOUT if a bounded wait ran out
  * since the last call, or EQAT_ERR_CUDA if the synchronisation failed.  If

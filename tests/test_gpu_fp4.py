@@ -1,0 +1,271 @@
+"""GPU parity of the microscaled 4-bit float operators against the CPU oracle.
+
+Codes, scale bytes, tensor scales and values must match exactly.  Products: with u = 2^-8
+the rounding of a bf16 result, and each of the K / 64 block products added to an fp32 sum
+within 2^-22 of the sum of magnitudes, |Y - ref| <= u |ref| + (K / 64 + 8) 2^-22
+sum |x w|; the backward's plain bf16 products likewise, with steps of 16."""
+import numpy as np
+import pytest
+import torch
+
+import weight_quantization_aware_b200 as eqat
+from oracle import fp4 as orc
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from weight_quantization_aware_b200 import build
+    build.build()
+    eqat.load_library()
+    assert torch.cuda.is_available()
+    yield
+    assert eqat.device_error() == 0
+
+
+def draw(N, K, dtype, seed, sigma=0.02):
+    rng = np.random.default_rng(seed)
+    w = rng.normal(size=(N, K)).astype(np.float32) * np.float32(sigma)
+    w[rng.random((N, K)) < 1e-2] *= 10
+    return torch.from_numpy(w).to(dtype)
+
+
+def f32(t):
+    return t.detach().cpu().float().numpy()
+
+
+def edge_values(N, K, dtype, seed):
+    """Values on and next to the borders between codes, zeros, blocks of one value, tiny
+    and huge blocks."""
+    rng = np.random.default_rng(seed)
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, 7.5, 0.0], np.float32)
+    w = rng.choice(mids, (N, K)) * rng.choice([-1.0, 1.0], (N, K))
+    w = (w * 2.0 ** rng.integers(-8, 5, (N, 1))).astype(np.float32)
+    w *= rng.choice(np.array([1, 1, 1, 1 + 2.0 ** -7, 1 - 2.0 ** -8, 1 + 2.0 ** -23, 1 - 2.0 ** -24], np.float32), (N, K))
+    if N > 4:
+        w[0] = 0.0
+        w[1, : K // 2] = -0.0
+        w[2] *= np.float32(2.0 ** -120)
+        w[3] *= np.float32(2.0 ** 100)
+        w[4, ::16] = 1e-40
+    return torch.from_numpy(w.astype(np.float32)).to(dtype)
+
+
+def check_pack(W, fmt, g):
+    N, K = W.shape
+    Wd = W.cuda()
+    gd = None if g is None else torch.tensor([g], dtype=torch.float32, device="cuda")
+    codes, scales = eqat.pack_fp4(Wd, fmt, tscale=gd)
+    c, s, v = orc.quantize(f32(W), fmt, g)
+    assert np.array_equal(codes.cpu().numpy(), orc.pack(c)), "codes"
+    assert np.array_equal(scales.cpu().numpy(), orc.tiles(s)), "scales"
+    want = torch.from_numpy(v.astype(np.float32)).to(W.dtype)
+    for got in (eqat.fake_quant_fp4(Wd, fmt, tscale=gd), eqat.dequant_fp4(codes, scales, fmt, tscale=gd, dtype=W.dtype)):
+        got = got.cpu()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(got.nan_to_num(0.0), want.nan_to_num(0.0)), "values"
+    return codes, scales, v
+
+
+SHAPES = [(1, 32), (3, 64), (8, 96), (128, 128), (129, 160), (301, 512), (40, 1056), (257, 4096)]
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("shape", SHAPES, ids=["x".join(map(str, s)) for s in SHAPES])
+def test_pack_matches_the_oracle(shape, dtype, fmt):
+    W = draw(*shape, dtype, sum(shape))
+    g = None
+    if fmt == "nv":
+        g = float(eqat.fp4_tensor_scale(W.cuda()).item())
+        assert np.float32(g) == orc.tensor_scale(f32(W))
+    check_pack(W, fmt, g)
+    check_pack(edge_values(*shape, dtype, 1), fmt, None if fmt == "mx" else 2.0 ** -4)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_any_tensor_scale(dtype):
+    """A tensor scale that is not a power of two: the same fp32 operations in the same order."""
+    for g in (0.0123, 3.7, 1.0, 1e-3):
+        W = draw(33, 256, dtype, 5)
+        gd = torch.tensor([g], dtype=torch.float32, device="cuda")
+        codes, scales = eqat.pack_fp4(W.cuda(), "nv", tscale=gd)
+        c, s, v = orc.quantize(f32(W), "nv", np.float32(g))
+        assert np.array_equal(codes.cpu().numpy(), orc.pack(c)) and np.array_equal(scales.cpu().numpy(), orc.tiles(s))
+        got = f32(eqat.dequant_fp4(codes, scales, "nv", tscale=gd, dtype=dtype)).astype(np.float64)
+        u = 2.0 ** -8 if dtype == torch.bfloat16 else 2.0 ** -24
+        assert (np.abs(got - v) <= np.abs(v) * (u + 2.0 ** -24)).all()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_blocks_with_nan_or_infinity(fmt):
+    W = draw(9, 128, torch.float32, 2)
+    W[2, 40] = float("nan")
+    W[5, 0] = float("inf")
+    W[8, 127] = -float("inf")
+    check_pack(W, fmt, 2.0 ** -10 if fmt == "nv" else None)
+
+
+def test_tensor_scale_edges():
+    for v, want in [(0.0, 2.0 ** -100), (2688.0, 1.0), (2688.0 * (1 + 2.0 ** -23), 2.0), (1e-38, 2.0 ** -100),
+                    (3e38, None)]:
+        W = torch.zeros(2, 64)
+        W[1, 5] = -v
+        W[0, 0] = float("nan")  # not a value
+        W[0, 1] = float("inf")
+        got = eqat.fp4_tensor_scale(W.cuda()).item()
+        assert got == (want if want is not None else float(orc.tensor_scale(W.numpy())))
+    assert eqat.fp4_tensor_scale(torch.zeros(0, 32, device="cuda")).item() == 2.0 ** -100
+
+
+def packed(W, fmt, g):
+    codes, scales = eqat.pack_fp4(W.cuda(), fmt, tscale=g)
+    return codes, scales
+
+
+def scale_of(t, fmt):
+    return eqat.fp4_tensor_scale(t.cuda()) if fmt == "nv" else None
+
+
+def values(t, fmt, g):
+    return orc.quantize(f32(t), fmt, None if g is None else np.float32(g.item()))[2]
+
+
+CASES = [(1, 8, 32), (1, 128, 256), (2, 136, 64), (7, 264, 320), (16, 512, 1024), (17, 128, 96), (33, 392, 4096),
+         (64, 72, 2048), (65, 1000, 512), (128, 256, 288), (129, 264, 320), (300, 520, 1184), (257, 8, 4096),
+         (515, 768, 2048)]
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("case", CASES, ids=["x".join(map(str, c)) for c in CASES])
+def test_linear_fwd(case, fmt):
+    M, N, K = case
+    X, W = draw(M, K, torch.bfloat16, 1, 1.0), draw(N, K, torch.bfloat16, 2)
+    gx, gw = scale_of(X, fmt), scale_of(W, fmt)
+    codes, scales = packed(W, fmt, gw)
+    Y = eqat.fp4_linear_fwd(X.cuda(), codes, scales, fmt, tscale=gw, x_tscale=gx)
+    xv, wv = values(X, fmt, gx), values(W, fmt, gw)
+    ref, mag = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    bound = 2.0 ** -8 * np.abs(ref) + (K / 64 + 8) * 2.0 ** -22 * mag + 1e-37
+    d = np.abs(f32(Y) - ref)
+    assert (d <= bound).all(), f"worst {np.max(d / bound):.3f} of the bound"
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("M", [3, 200])
+def test_linear_fwd_keeps_nan_blocks_to_their_rows(M, fmt):
+    N, K = 136, 192
+    X, W = draw(M, K, torch.bfloat16, 1, 1.0), draw(N, K, torch.bfloat16, 2)
+    X[1, 70] = float("nan")
+    W[130, 5] = float("inf")
+    g = torch.tensor([2.0 ** -8], device="cuda") if fmt == "nv" else None
+    codes, scales = packed(W, fmt, g)
+    Y = eqat.fp4_linear_fwd(X.cuda(), codes, scales, fmt, tscale=g, x_tscale=g).cpu()
+    want = torch.zeros(M, N, dtype=torch.bool)
+    want[1] = True
+    want[:, 130] = True
+    assert torch.equal(torch.isnan(Y), want)
+
+
+BWD = [(1, 8, 32), (5, 136, 96), (130, 264, 320), (300, 128, 1024)]
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("case", BWD, ids=["x".join(map(str, c)) for c in BWD])
+def test_linear_bwd(case, fmt):
+    M, N, K = case
+    X, W, dY = draw(M, K, torch.bfloat16, 1, 1.0), draw(N, K, torch.bfloat16, 2), draw(M, N, torch.bfloat16, 3, 0.01)
+    gx, gw = scale_of(X, fmt), scale_of(W, fmt)
+    codes, scales = packed(W, fmt, gw)
+    dX, dW = eqat.fp4_linear_bwd(X.cuda(), codes, scales, dY.cuda(), fmt, tscale=gw, x_tscale=gx)
+    xv, wv, dy = values(X, fmt, gx), values(W, fmt, gw), f32(dY).astype(np.float64)
+    for got, a, b, n in ((dX, dy, wv, N), (dW, dy.T, xv, M)):
+        ref, mag = a @ b, np.abs(a) @ np.abs(b)
+        bound = 2.0 ** -8 * np.abs(ref) + (n / 16 + 8) * 2.0 ** -22 * mag + 1e-37
+        d = np.abs(f32(got) - ref)
+        assert (d <= bound).all(), f"worst {np.max(d / bound):.3f} of the bound"
+    only, none = eqat.fp4_linear_bwd(X.cuda(), codes, scales, dY.cuda(), fmt, tscale=gw, x_tscale=gx, need_dw=False)
+    assert none is None and torch.equal(only, dX)
+
+
+def test_backward_matches_differences():
+    """The product is linear in each packed operand: dX against the change of sum(dY Y)
+    when a block of X moves along the packed grid by whole codes (both exact)."""
+    M, N, K, fmt = 4, 64, 64, "mx"
+    X = torch.full((M, K), 1.0, dtype=torch.bfloat16)
+    X[:, ::32] = 4.0  # every block's scale stays 1
+    W, dY = draw(N, K, torch.bfloat16, 4), draw(M, N, torch.bfloat16, 5)
+    codes, scales = packed(W, fmt, None)
+    dX, _ = eqat.fp4_linear_bwd(X.cuda(), codes, scales, dY.cuda(), fmt)
+    up, dn = X.clone(), X.clone()
+    up[2, 7], dn[2, 7] = 1.5, 0.5
+    wv = values(W, fmt, None)
+    dy = f32(dY).astype(np.float64)
+    num = (dy * (values(up, fmt, None) @ wv.T - values(dn, fmt, None) @ wv.T)).sum()
+    assert abs(num - float(dX[2, 7])) <= 2.0 ** -7 * abs(num) + 1e-6 * np.abs(dy[2]) @ np.abs(wv[:, 7])
+
+
+def test_workspaces_outputs_and_empty_calls():
+    M, N, K, fmt = 20, 64, 128, "nv"
+    X, W = draw(M, K, torch.bfloat16, 1, 1.0).cuda(), draw(N, K, torch.bfloat16, 2)
+    g = scale_of(W, fmt)
+    codes, scales = packed(W, fmt, g)
+    want = eqat.fp4_linear_fwd(X, codes, scales, fmt, tscale=g)
+    ws = eqat.fp4_workspace(M, N, K, fmt).fill_(255)
+    Y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
+    got = eqat.fp4_linear_fwd(X, codes, scales, fmt, tscale=g, ws=ws, Y=Y)
+    assert got.data_ptr() == Y.data_ptr() and torch.equal(got, want)
+    with pytest.raises(eqat.EqatError):
+        eqat.fp4_linear_fwd(X, codes, scales, fmt, tscale=g, ws=ws[:256])
+    assert eqat.fp4_linear_fwd(X[:0], codes, scales, fmt).shape == (0, N)
+    dX, dW = eqat.fp4_linear_bwd(X[:0], codes, scales, torch.empty(0, N, dtype=torch.bfloat16, device="cuda"), fmt)
+    assert dX.shape == (0, K) and dW.shape == (N, K) and not dW.any()
+    with pytest.raises(eqat.EqatError):
+        eqat.fp4_linear_fwd(X, codes, eqat.pack_fp4(W.cuda(), "mx")[1], "mx", tscale=g)
+
+
+def test_graph_and_side_stream():
+    M, N, K, fmt = 9, 264, 512, "nv"
+    X, W = draw(M, K, torch.bfloat16, 1, 1.0).cuda(), draw(N, K, torch.bfloat16, 2).cuda()
+    g = eqat.fp4_tensor_scale(W)
+    codes, scales = eqat.pack_fp4(W, fmt, tscale=g)
+    want = eqat.fp4_linear_fwd(X, codes, scales, fmt, tscale=g)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = eqat.fp4_linear_fwd(X, codes, scales, fmt, tscale=g)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g2 = eqat.fp4_tensor_scale(W)
+        c2, s2 = eqat.pack_fp4(W, fmt, tscale=g2)
+        Y = eqat.fp4_linear_fwd(X, c2, s2, fmt, tscale=g2)
+    X.mul_(2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(Y, eqat.fp4_linear_fwd(X, codes, scales, fmt, tscale=g))
+
+
+def test_a_distillation_step_through_a_packed_output_layer():
+    """Teacher's logits -> alternatives -> the loss of a packed student -> its gradients,
+    against the same chain in fp64 with the kernels' packed values and bf16 logits."""
+    from oracle import rows
+    M, V, K, k, fmt = 70, 1024, 256, 16, "nv"
+    X, W = draw(M, K, torch.bfloat16, 1, 1.0).cuda(), draw(V, K, torch.bfloat16, 2, 0.1)
+    T = (X.float() @ W.cuda().float().t()).to(torch.bfloat16)
+    lp, ent, ids, tlp = eqat.token_logprobs(T, torch.arange(M, device="cuda"), top_k=k)
+    gw, gx = eqat.fp4_tensor_scale(W.cuda()), eqat.fp4_tensor_scale(X)
+    codes, scales = eqat.pack_fp4(W.cuda(), fmt, tscale=gw)
+    Y = eqat.fp4_linear_fwd(X, codes, scales, fmt, tscale=gw, x_tscale=gx)
+    w = torch.full((M,), 1.0 / M, device="cuda")
+    loss, dY = eqat.distill_topk_step(Y, ids, tlp, weight=w, tail=True)
+    dX, dW = eqat.fp4_linear_bwd(X, codes, scales, dY, fmt, tscale=gw, x_tscale=gx)
+    want_l, want_g = rows.distill_topk(f32(Y), ids.cpu().numpy(), f32(tlp), f32(w), 1.0, True)
+    assert np.allclose(f32(loss), want_l, rtol=1e-4, atol=1e-7)
+    xv, wv, dy = values(X, fmt, gx), values(W, fmt, gw), f32(dY).astype(np.float64)
+    assert np.abs(dy - want_g).max() <= 2.0 ** -8 * np.abs(want_g).max() + 1e-9
+    for got, a, b, n in ((dX, dy, wv, V), (dW, dy.T, xv, M)):
+        ref, mag = a @ b, np.abs(a) @ np.abs(b)
+        assert (np.abs(f32(got) - ref) <= 2.0 ** -8 * np.abs(ref) + (n / 16 + 8) * 2.0 ** -22 * mag).all()

@@ -1,0 +1,288 @@
+"""GPU parity of token_logprobs and distill_topk_* against the fp64 oracle.
+
+Tolerances, derived once.  A thread adds about V / 512 terms of one sign into each of two
+fp32 sums and the block joins 512 of them in 13 steps, so S has a relative error of at
+most (V / 512 + 16) 2^-24 from the additions; each term 2^y carries 2^-22 from ex2 and,
+from two roundings of y, |y| 2^-23 ln 2, which weighted by 2^y stays below 2^-23.  So
+ln S is within tol(V) = (V / 512 + 32) 2^-24 + 2^-21, absolutely.  Values that are
+rounded to fp32 at the end add 2^-24 of themselves.
+"""
+import numpy as np
+import pytest
+import torch
+
+import weight_quantization_aware_b200 as eqat
+from oracle import rows as orc
+
+pytestmark = pytest.mark.gpu
+HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from weight_quantization_aware_b200 import build
+    build.build()
+    eqat.load_library()
+    assert torch.cuda.is_available()
+    yield
+    assert eqat.device_error() == 0
+
+
+def tol(V):
+    return (V / 512 + 32) * 2.0 ** -24 + 2.0 ** -21
+
+
+def make(T, V, dtype, seed, ld=None):
+    rng = np.random.default_rng(seed)
+    x = rng.normal(size=(T, V)) * 3
+    x[np.arange(T), rng.integers(0, V, T)] += 8 * rng.random(T)
+    t = torch.from_numpy(x).to(dtype)
+    if ld is None:
+        return t.cuda()
+    wide = torch.full((T, ld), float("nan"), dtype=dtype)  # what lies past a row is never read
+    wide[:, :V] = t
+    return wide.cuda()[:, :V]
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def same(got, want, bound, name):
+    """Equal where not finite, within `bound` elsewhere."""
+    got, want = np.asarray(got, np.float64), np.asarray(want, np.float64)
+    assert got.shape == want.shape, name
+    fin = np.isfinite(want)
+    assert np.array_equal(got[~fin], want[~fin], equal_nan=True), f"{name}: non-finite values differ"
+    d = np.abs(got[fin] - want[fin])
+    b = np.broadcast_to(bound, want.shape)[fin]
+    assert np.isfinite(got[fin]).all() and (d <= b).all(), f"{name}: worst {np.max(d / b):.3f} of the bound"
+
+
+def check_logprobs(x, targets, k, tau=1.0):
+    lp, ent, ids, top = eqat.token_logprobs(x, targets, top_k=k, temperature=tau)
+    V = x.shape[1]
+    xn = f64(x)
+    w_lp, w_ent, w_ids, w_top = orc.token_logprobs(xn, targets.cpu().numpy(), k, tau)
+    e = tol(V)
+    same(f64(lp), w_lp, e + np.abs(np.nan_to_num(w_lp, neginf=0)) * 2.0 ** -23, "logprob")
+    # H = ln S - ln 2 A / S: A's relative error is S's plus one rounding of each y
+    span = np.abs(np.nan_to_num(w_ent)) + np.log(V)  # bounds E|y| ln 2
+    same(f64(ent), w_ent, e * (2 + 3 * span), "entropy")
+    if k:
+        assert np.array_equal(ids.cpu().numpy(), w_ids), "ids"
+        same(f64(top), w_top, e + np.abs(np.nan_to_num(w_top, neginf=0)) * 2.0 ** -23, "top")
+    else:
+        assert ids is None and top is None
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,V,k", [(1, 1, 1), (1, 2, 0), (3, 7, 7), (2, 33, 128), (5, 1000, 5), (4, 2049, 128),
+                                   (9, 32000, 1), (3, 50001, 64), (700, 513, 20), (2, 131075, 100)])
+def test_logprobs(T, V, k, dtype):
+    x = make(T, V, dtype, T * V)
+    g = torch.Generator().manual_seed(3)
+    check_logprobs(x, torch.randint(0, V, (T,), generator=g).cuda(), min(k, 128))
+
+
+@pytest.mark.parametrize("tau", [0.25, 3.0, 1e-6, 1e6])
+def test_logprobs_temperature(tau):
+    x = make(6, 4097, torch.float32, 1)
+    t = torch.arange(6, device="cuda")
+    lp, ent, _, _ = eqat.token_logprobs(x, t, temperature=tau)
+    w_lp, w_ent, _, _ = orc.token_logprobs(f64(x), t.cpu().numpy(), 0, tau)
+    # every y is rounded twice: at an extreme temperature the error of the largest
+    # scaled logit counts, 2^-23 of it
+    big = np.abs(w_lp) * 2.0 ** -22
+    same(f64(lp), w_lp, tol(4097) + big, "logprob")
+    same(f64(ent), w_ent, tol(4097) * (2 + 3 * (w_ent + np.log(4097))), "entropy")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_logprobs_strides_masks_and_bad_rows(dtype):
+    T, V = 12, 3001
+    for ld in (3001, 3002, 3008, 4000):
+        x = make(T, V, dtype, ld, ld)
+        lowest = torch.finfo(dtype).min
+        x[1, 5:] = -float("inf")           # five entries left
+        x[2] = -float("inf")               # nothing left
+        x[3, 100:] = lowest                # masked by the type's lowest value
+        x[4] = lowest                      # a whole row of it: uniform
+        x[5, 17] = float("nan")
+        x[6, 18] = float("inf")
+        x[7] = 0.0                         # all equal
+        x[8, ::2] = 0.0                    # ties of both zeros
+        x[8, 1::2] = -0.0
+        x[9, 1:] = -float("inf")           # one entry left
+        t = torch.tensor([0, 3, 3, 200, 1, 0, 0, 9, 9, 0, -100, V], device="cuda")
+        check_logprobs(x, t, 40)
+        check_logprobs(x, torch.full((T,), -1, device="cuda"), 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_top_k_of_uneven_and_tied_rows(dtype):
+    """Rows whose candidates overflow the selection's buffer: large values in one stride
+    of the walk, few distinct values, everything equal but a handful."""
+    V = 20011
+    x = make(6, V, dtype, 2)
+    x[0] = 1.0
+    x[1] = (torch.arange(V) % 3).to(dtype)
+    x[2] = 1.0
+    x[2, torch.tensor([19999, 7, 12345])] = 2.0
+    x[2, 20000:] = 0.5
+    x[3] = torch.sort(x[3])[0]
+    x[4] = torch.round(x[4])
+    x[5] = -5.0
+    x[5, V - 1] = -4.0
+    for k in (1, 3, 64, 128):
+        check_logprobs(x, torch.arange(6, device="cuda"), k)
+
+
+def check_distill(x, ids, tlp, w, tau, tail):
+    V = x.shape[1]
+    want_l, want_g = orc.distill_topk(f64(x), ids.cpu().numpy(), f64(tlp), None if w is None else f64(w), tau, tail)
+    loss, grad = eqat.distill_topk_step(x, ids, tlp, weight=w, temperature=tau, tail=tail)
+    wn = np.ones(x.shape[0]) if w is None else np.abs(f64(w))
+    e = 2 * tol(V)  # ln S, and ln of the sum outside the slots
+    # the loss multiplies those by masses that add up to 1; the largest |ln p| by 2^-22
+    same(f64(loss), want_l, wn * 2 * e + np.abs(np.nan_to_num(want_l, posinf=0)) * 2.0 ** -22 + 1e-37, "loss")
+    # a gradient is a difference of masses, each with S's relative error, 2^-21, and
+    # |y| 2^-23 of its exponent (|y| <= 150 where 2^y is not 0)
+    xz = f64(x) / tau
+    with np.errstate(invalid="ignore", over="ignore"):
+        z = xz - np.max(np.where(np.isnan(xz), -np.inf, xz), 1, keepdims=True)
+        p = np.nan_to_num(np.exp(z) / np.exp(z).sum(1, keepdims=True))
+    mag = 2 * p + np.abs(np.nan_to_num(want_g)) / np.maximum(wn[:, None], 1e-30) * tau
+    rel = e + 2.0 ** -20 + 150 * 2.0 ** -23
+    bound = wn[:, None] / tau * mag * rel + np.abs(np.nan_to_num(want_g)) * (HALF[x.dtype] + 2.0 ** -22) + 1e-37
+    same(f64(grad), want_g, bound, "gradient")
+    # the separate calls give the same bits
+    assert torch.equal(eqat.distill_topk_fwd(x, ids, tlp, weight=w, temperature=tau, tail=tail).nan_to_num(7.0), loss.nan_to_num(7.0))
+    dl = torch.ones(x.shape[0], device="cuda") if w is None else w
+    g2 = eqat.distill_topk_bwd(x, ids, tlp, dl, temperature=tau, tail=tail)
+    assert torch.equal(g2.nan_to_num(7.0), grad.nan_to_num(7.0))
+    return loss, grad
+
+
+def teacher(x, k, seed, tau=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    y = x.float() + torch.randn(x.shape, generator=g, device="cuda")
+    t = torch.zeros(x.shape[0], dtype=torch.int64, device="cuda")
+    _, _, ids, tlp = eqat.token_logprobs(y, t, top_k=k, temperature=tau)
+    return ids, tlp
+
+
+@pytest.mark.parametrize("tail", [False, True], ids=["renorm", "tail"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T,V,k,tau", [(1, 1, 1, 1.0), (2, 5, 5, 1.0), (3, 9, 4, 2.0), (4, 1000, 1, 0.7),
+                                       (700, 515, 16, 1.0), (5, 32000, 128, 2.0), (2, 131075, 32, 1.0)])
+def test_distill(T, V, k, tau, dtype, tail):
+    x = make(T, V, dtype, T + V)
+    ids, tlp = teacher(x, k, V, tau)
+    w = torch.linspace(0.0, 1.0, T, device="cuda") if T > 1 else None
+    check_distill(x, ids, tlp, w, tau, tail)
+
+
+@pytest.mark.parametrize("tail", [False, True], ids=["renorm", "tail"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_distill_edges(dtype, tail):
+    T, V, k = 14, 2003, 6
+    for ld in (2003, 2004, 2048):
+        x = make(T, V, dtype, ld, ld)
+        clean = make(T, V, dtype, ld)
+        ids, tlp = teacher(clean, k, 9)
+        inf = float("inf")
+        ids[1, 2:] = -1                        # empty slots
+        ids[2] = -1                            # a teacher without alternatives
+        tlp[3] = -inf                          # alternatives without mass
+        x[4] = -inf                            # a student without entries
+        x[5, int(ids[5, 1])] = -inf            # a masked entry under a slot with mass
+        ids[6, 4] = ids[6, 0]                  # an id given twice, and three times
+        ids[7, 1] = ids[7, 2] = ids[7, 5]
+        ids[8, 0] = V                          # outside the vocabulary
+        x[9, 3] = float("nan")
+        x[10, 3] = inf
+        tlp[11, 0] = inf
+        keep = x[12, ids[12]].clone()          # nothing outside the slots
+        x[12] = -inf
+        x[12, ids[12]] = keep
+        x[13] = torch.finfo(dtype).min         # uniform
+        check_distill(x, ids, tlp, None, 1.0, tail)
+        w = torch.ones(T, device="cuda")
+        w[9] = w[8] = 0.0                      # rows of weight 0 are not looked at
+        w[3] = -2.0
+        check_distill(x, ids, tlp, w, 1.5, tail)
+
+
+def test_distill_tail_does_not_cancel():
+    """Nearly all mass on the slots: the student's mass outside them is far below 2^-24."""
+    V, k = 5000, 3
+    x = make(3, V, torch.float32, 4)
+    x[:, :k] += 40.0
+    ids = torch.arange(k, device="cuda").repeat(3, 1)
+    tlp = torch.log(torch.tensor([[0.5, 0.3, 0.1], [0.4, 0.4, 0.2 - 1e-4], [0.2, 0.2, 0.2]], device="cuda"))
+    check_distill(x, ids, tlp, None, 1.0, True)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_distill_in_place_and_padding_left_alone(dtype):
+    T, V, ld = 33, 1001, 1024
+    wide = torch.randn(T, ld, device="cuda").to(dtype)
+    pad = wide[:, V:].clone()
+    x = wide[:, :V]
+    ids, tlp = teacher(x, 8, 1)
+    # same strides, same order of additions: bit for bit
+    want = eqat.distill_topk_bwd(x, ids, tlp, torch.ones(T, device="cuda"), tail=True)
+    assert want.stride() == x.stride()
+    out = torch.full((T, ld), 7.0, dtype=dtype, device="cuda")
+    eqat.distill_topk_bwd(x, ids, tlp, torch.ones(T, device="cuda"), tail=True, dlogits=out[:, :V])
+    assert torch.equal(out[:, :V], want) and (out[:, V:] == 7.0).all()
+    got = eqat.distill_topk_bwd(x, ids, tlp, torch.ones(T, device="cuda"), tail=True, dlogits=x)
+    assert got.data_ptr() == x.data_ptr()
+    assert torch.equal(x, want) and torch.equal(wide[:, V:], pad)
+
+
+def test_distill_gradient_matches_differences():
+    """The kernel's gradient against central differences of the kernel's own fp32 loss,
+    summed along a random direction: h = 2^-4 leaves a third-order error of about
+    h^2 |d|^3 / 6 per row and a rounding error of 2 tol / h."""
+    T, V, k = 8, 257, 12
+    x = make(T, V, torch.float32, 8)
+    ids, tlp = teacher(x, k, 2)
+    d = torch.nn.functional.normalize(torch.randn(T, V, device="cuda"), dim=1)
+    h = 2.0 ** -4
+    for tail in (False, True):
+        up = eqat.distill_topk_fwd(x + h * d, ids, tlp, tail=tail).double()
+        dn = eqat.distill_topk_fwd(x - h * d, ids, tlp, tail=tail).double()
+        g = eqat.distill_topk_bwd(x, ids, tlp, torch.ones(T, device="cuda"), tail=tail)
+        num, ana = (up - dn) / (2 * h), (g.double() * d.double()).sum(1)
+        assert (num - ana).abs().max().item() < h * h / 6 + 2 * tol(V) / h
+
+
+def test_rows_on_a_side_stream_and_in_a_captured_graph():
+    T, V, k = 40, 4099, 9
+    x = make(T, V, torch.bfloat16, 3)
+    tg = torch.arange(T, device="cuda")
+    want = eqat.token_logprobs(x, tg, top_k=k)
+    want_l, want_g = eqat.distill_topk_step(x, want[2], want[3], tail=True)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = eqat.token_logprobs(x, tg, top_k=k)
+        l, g = eqat.distill_topk_step(x, got[2], got[3], tail=True)
+    torch.cuda.current_stream().wait_stream(s)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert torch.equal(l, want_l) and torch.equal(g, want_g)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = eqat.token_logprobs(x, tg, top_k=k)
+        l, g = eqat.distill_topk_step(x, got[2], got[3], tail=True)
+    x.copy_(make(T, V, torch.bfloat16, 4))
+    graph.replay()
+    torch.cuda.synchronize()
+    again = eqat.token_logprobs(x, tg, top_k=k)
+    for a, b in zip(got, again):
+        assert torch.equal(a, b)
+    l2, g2 = eqat.distill_topk_step(x, again[2], again[3], tail=True)
+    assert torch.equal(l, l2) and torch.equal(g, g2)

@@ -22,6 +22,8 @@ EQAT_F32 = 0
 EQAT_BF16 = 1
 EQAT_F16 = 2  # step sizes of the E2E-QP calls only
 EQAT_GRAD_CLAMP_PASS = 1
+EQAT_DISTILL_TAIL = 1
+EQAT_TOP_MAX = 128  # alternatives per row of token_logprobs and distill_topk_*
 EQAT_ERR_TIMEOUT = 8
 
 _lib = None
@@ -63,6 +65,14 @@ def load_library():
         "eqat_dq_linear_bwd": [P, I, P, P, P, I, P, P, P, P, I64, I64, I64, I, I, P, SZ, I, P],
         "eqat_fq_linear_fwd_mse": [P, P, I, P, P, P, P, P, I64, I64, I64, I, I, P, SZ, P],
         "eqat_adamw_step": [P, I, P, I, I64, P],
+        "eqat_token_logprobs": [P, I, I64, I64, I64, P, ctypes.c_double, I, P, P, P, P, P],
+        "eqat_distill_topk": [P, I, I64, I64, I64, P, P, I, ctypes.c_double, U32, P, P, P, P],
+        "eqat_fp4_tensor_scale": [P, I, I64, P, P],
+        "eqat_pack_fp4": [P, I, I64, I64, I, P, P, P, P],
+        "eqat_fake_quant_fp4": [P, I, I64, I64, I, P, P, P],
+        "eqat_dequant_fp4": [P, P, I64, I64, I, P, P, I, P],
+        "eqat_fp4_linear_fwd": [P, P, P, I, P, P, P, I64, I64, I64, P, SZ, P],
+        "eqat_fp4_linear_bwd": [P, P, P, I, P, P, P, P, P, I64, I64, I64, P, SZ, P],
         "eqat_device_error": [P, P],
         "eqat_selftest_bounded_wait": [I64, P],
     }
@@ -79,6 +89,10 @@ def load_library():
     lib.eqat_cosine_lr.restype = ctypes.c_double
     lib.eqat_workspace_bytes.argtypes = [I64, I64, I64, I, I, I]
     lib.eqat_workspace_bytes.restype = SZ
+    lib.eqat_fp4_scale_bytes.argtypes = [I64, I64, I]
+    lib.eqat_fp4_scale_bytes.restype = SZ
+    lib.eqat_fp4_workspace_bytes.argtypes = [I64, I64, I64, I, I]
+    lib.eqat_fp4_workspace_bytes.restype = SZ
     _lib = lib
     return lib
 
@@ -482,6 +496,241 @@ def fq_linear_fwd_mse(X, W, s, z, T, bits, group, ws=None, dY=None, loss=None):
     _call("eqat_fq_linear_fwd_mse", _p(X), _p(W), _dt(X), _p(s), _p(z), _p(T), _p(dY), _p(loss), M, N, K, bits,
           group, _p(ws), ws.numel(), _stream())
     return dY, loss
+
+
+# ---------------------------------------------------------------- rows of logits
+
+
+def _here(*ts):
+    """Refuses tensors that are not on the current CUDA device, whose stream the call
+    goes to."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _rows(x, name):
+    """(T, V, ld) of logits [T, V] whose rows are dense and ld elements apart."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be 2-D [T, V], got shape {tuple(x.shape)}")
+    T, V = x.shape
+    ld = x.stride(0) if T > 1 else V
+    if (V > 1 and x.stride(1) != 1) or ld < V:
+        raise ValueError(f"{name} must have dense rows that do not overlap, got strides {x.stride()}")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return T, V, ld
+
+
+def token_logprobs(logits, targets, top_k=0, temperature=1.0):
+    """Log probabilities of `targets` (int64 [T]; negative: not scored) under the rows of
+    logits [T, V] (bf16 or fp32, rows may be strided), with each row's entropy and top
+    alternatives: returns (logprob [T], entropy [T], top_ids int64 [T, top_k],
+    top_logprobs [T, top_k]), fp32 except the ids; the last two are None where top_k is
+    0.  Equal logits rank by index; alternatives that a row lacks have id -1."""
+    _shape(targets, "targets", (logits.shape[0],))
+    T, V, ld = _rows(logits, "logits")
+    _req(targets, "targets", torch.int64)
+    _here(logits, targets)
+    f32 = dict(dtype=torch.float32, device=logits.device)
+    lp, ent = torch.empty(T, **f32), torch.empty(T, **f32)
+    ids = top = None
+    if top_k > 0:
+        ids = torch.empty((T, top_k), dtype=torch.int64, device=logits.device)
+        top = torch.empty((T, top_k), **f32)
+    _call("eqat_token_logprobs", _p(logits), _dt(logits), ld, T, V, _p(targets), temperature, top_k, _p(lp),
+          _p(ent), _p(ids), _p(top), _stream())
+    return lp, ent, ids, top
+
+
+def _distill(logits, ids, tlp, weight, temperature, tail, want_loss, want_grad, dlogits):
+    if ids.dim() != 2:
+        raise ValueError(f"ids must be 2-D [T, k], got shape {tuple(ids.shape)}")
+    k = ids.shape[1]
+    _shape(ids, "ids", (logits.shape[0], k))
+    _shape(tlp, "tlp", (logits.shape[0], k))
+    _shape(weight, "weight", (logits.shape[0],))
+    _shape(dlogits, "dlogits", logits.shape)
+    T, V, ld = _rows(logits, "logits")
+    _req(ids, "ids", torch.int64); _req(tlp, "tlp", torch.float32)
+    if weight is not None:
+        _req(weight, "weight", torch.float32)
+    if want_grad:
+        if dlogits is None:
+            dlogits = torch.empty((T, ld), dtype=logits.dtype, device=logits.device)
+            dlogits = dlogits if ld == V else dlogits[:, :V]
+        elif _rows(dlogits, "dlogits")[2] != ld:
+            raise ValueError("dlogits must have the strides of logits")
+        elif dlogits.dtype != logits.dtype:
+            raise TypeError(f"dlogits must be {logits.dtype}, got {dlogits.dtype}")
+    loss = torch.empty(T, dtype=torch.float32, device=logits.device) if want_loss else None
+    _here(logits, ids, tlp, weight, dlogits)
+    _call("eqat_distill_topk", _p(logits), _dt(logits), ld, T, V, _p(ids), _p(tlp), k, temperature,
+          EQAT_DISTILL_TAIL if tail else 0, _p(weight), _p(loss), _p(dlogits), _stream())
+    return loss, dlogits
+
+
+def distill_topk_fwd(logits, ids, tlp, weight=None, temperature=1.0, tail=False):
+    """Distillation loss [T] (fp32) of a student's logits [T, V] against a teacher's
+    alternatives: ids int64 [T, k] (negative: empty slot) and their log probabilities
+    tlp fp32 [T, k], as token_logprobs gives them.  tail=False renormalises the teacher
+    over the slots; tail=True compares what it has outside them with the student's mass
+    outside them.  weight fp32 [T] multiplies each row's loss; a row of weight 0 is
+    skipped."""
+    return _distill(logits, ids, tlp, weight, temperature, tail, True, False, None)[0]
+
+
+def distill_topk_bwd(logits, ids, tlp, dloss, temperature=1.0, tail=False, dlogits=None):
+    """Gradient of distill_topk_fwd's unweighted loss with respect to the logits, where
+    dloss fp32 [T] arrives at it.  dlogits, if given, receives it and may be the logits
+    themselves (same strides)."""
+    return _distill(logits, ids, tlp, dloss, temperature, tail, False, True, dlogits)[1]
+
+
+def distill_topk_step(logits, ids, tlp, weight=None, temperature=1.0, tail=False, dlogits=None):
+    """(loss, dlogits) in one pass over the logits: loss = weight * L per row, and
+    dlogits = d(sum of loss) / d(logits)."""
+    return _distill(logits, ids, tlp, weight, temperature, tail, True, True, dlogits)
+
+
+# ---------------------------------------------------------------- microscaled 4-bit floats
+
+FP4_BLOCK = {"mx": 32, "nv": 16}
+
+
+def _fmt(fmt):
+    if fmt not in FP4_BLOCK:
+        raise ValueError(f"fmt must be 'mx' or 'nv', got {fmt!r}")
+    return 1 if fmt == "nv" else 0
+
+
+def _tscale(g, name="tscale"):
+    if g is not None:
+        _shape(g, name, (1,))
+        _req(g, name, torch.float32)
+
+
+def fp4_scale_shape(N: int, K: int, fmt: str):
+    """Shape of the scale tiles of an [N, K] matrix: tiles of 128 rows by 4 blocks."""
+    return (-(-N // 128), -(-(K // FP4_BLOCK[fmt]) // 4), 512)
+
+
+def _fp4_matrix(W, name="W"):
+    if W.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got shape {tuple(W.shape)}")
+    if W.shape[1] % 32:
+        raise ValueError(f"{name} has shape {tuple(W.shape)}: K must be a multiple of 32")
+    return W.shape
+
+
+def fp4_tensor_scale(W, out=None):
+    """The tensor scale of the "nv" format: the smallest power of two g with
+    max|W| <= 6 * 448 * g, one fp32 value on the device."""
+    _fp4_matrix(W)
+    _shape(out, "out", (1,))
+    _req(W, "W")
+    out = torch.empty(1, dtype=torch.float32, device=W.device) if out is None else _req(out, "out", torch.float32)
+    _here(W, out)
+    _call("eqat_fp4_tensor_scale", _p(W), _dt(W), W.numel(), _p(out), _stream())
+    return out
+
+
+def pack_fp4(W, fmt, tscale=None, codes=None, scales=None):
+    """Packs W [N, K] (bf16 or fp32) into 4-bit floats: returns (codes uint8 [N, K/2],
+    scales uint8 tiles of fp4_scale_shape(N, K, fmt)).  tscale: the tensor scale of "nv"."""
+    f = _fmt(fmt)
+    N, K = _fp4_matrix(W)
+    _shape(codes, "codes", (N, K // 2)); _shape(scales, "scales", fp4_scale_shape(N, K, fmt))
+    _req(W, "W")
+    _tscale(tscale)
+    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device) if codes is None else \
+        _req(codes, "codes", torch.uint8)
+    scales = torch.empty(fp4_scale_shape(N, K, fmt), dtype=torch.uint8, device=W.device) if scales is None else \
+        _req(scales, "scales", torch.uint8)
+    _here(W, tscale, codes, scales)
+    _call("eqat_pack_fp4", _p(W), _dt(W), N, K, f, _p(tscale), _p(codes), _p(scales), _stream())
+    return codes, scales
+
+
+def fake_quant_fp4(W, fmt, tscale=None, W_hat=None):
+    """The values that pack_fp4 would store, in W's dtype."""
+    f = _fmt(fmt)
+    N, K = _fp4_matrix(W)
+    _shape(W_hat, "W_hat", (N, K))
+    _req(W, "W")
+    _tscale(tscale)
+    W_hat = torch.empty_like(W) if W_hat is None else _req(W_hat, "W_hat", W.dtype)
+    _here(W, tscale, W_hat)
+    _call("eqat_fake_quant_fp4", _p(W), _dt(W), N, K, f, _p(tscale), _p(W_hat), _stream())
+    return W_hat
+
+
+def dequant_fp4(codes, scales, fmt, tscale=None, dtype=torch.bfloat16, out=None):
+    """The values of packed codes [N, K/2], [N, K] of `dtype` (or into `out`)."""
+    f = _fmt(fmt)
+    if codes.dim() != 2:
+        raise ValueError(f"codes must be 2-D [N, K/2], got shape {tuple(codes.shape)}")
+    N, K = codes.shape[0], codes.shape[1] * 2
+    _shape(scales, "scales", fp4_scale_shape(N, K, fmt)); _shape(out, "out", (N, K))
+    _req(codes, "codes", torch.uint8); _req(scales, "scales", torch.uint8)
+    _tscale(tscale)
+    out = torch.empty((N, K), dtype=dtype, device=codes.device) if out is None else _req(out, "out")
+    _here(codes, scales, tscale, out)
+    _call("eqat_dequant_fp4", _p(codes), _p(scales), N, K, f, _p(tscale), _p(out), _dt(out), _stream())
+    return out
+
+
+def fp4_workspace(M, N, K, fmt, backward=False, device=None) -> torch.Tensor:
+    """A uint8 CUDA buffer for fp4_linear_fwd (or, with backward, fp4_linear_bwd)."""
+    n = int(load_library().eqat_fp4_workspace_bytes(M, N, K, _fmt(fmt), int(backward)))
+    return torch.empty(max(n, 1), dtype=torch.uint8, device=device or "cuda")
+
+
+def _fp4_linear(X, codes, scales, fmt, tscale, x_tscale, **mn):
+    f = _fmt(fmt)
+    M, K = _fp4_matrix(X, "X")
+    if codes.dim() != 2:
+        raise ValueError(f"codes must be 2-D [N, K/2], got shape {tuple(codes.shape)}")
+    N = codes.shape[0]
+    _shape(codes, "codes", (N, K // 2)); _shape(scales, "scales", fp4_scale_shape(N, K, fmt))
+    for name, (t, shape) in mn.items():
+        _shape(t, name, {"MN": (M, N), "MK": (M, K), "NK": (N, K)}[shape])
+        if t is not None:
+            _req(t, name, torch.bfloat16)
+    _req(X, "X", torch.bfloat16); _req(codes, "codes", torch.uint8); _req(scales, "scales", torch.uint8)
+    _tscale(tscale); _tscale(x_tscale, "x_tscale")
+    return f, M, N, K
+
+
+def fp4_linear_fwd(X, codes, scales, fmt, tscale=None, x_tscale=None, ws=None, Y=None):
+    """Y = X_hat W_hat^T with both operands in 4-bit floats: X [M, K] bf16 is packed in
+    the call (tensor scale x_tscale), W comes from pack_fp4 (tensor scale tscale)."""
+    f, M, N, K = _fp4_linear(X, codes, scales, fmt, tscale, x_tscale, Y=(Y, "MN"))
+    Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device) if Y is None else Y
+    ws = fp4_workspace(M, N, K, fmt, False, X.device) if ws is None else _req(ws, "ws", torch.uint8)
+    _here(X, codes, scales, tscale, x_tscale, ws, Y)
+    _call("eqat_fp4_linear_fwd", _p(X), _p(codes), _p(scales), f, _p(x_tscale), _p(tscale), _p(Y), M, N, K,
+          _p(ws), ws.numel(), _stream())
+    return Y
+
+
+def fp4_linear_bwd(X, codes, scales, dY, fmt, tscale=None, x_tscale=None, need_dx=True, need_dw=True, ws=None,
+                   out=None):
+    """Straight-through backward of fp4_linear_fwd: returns (dX = dY W_hat,
+    dW = dY^T X_hat), None where not requested."""
+    dX, dW = (None, None) if out is None else out
+    f, M, N, K = _fp4_linear(X, codes, scales, fmt, tscale, x_tscale, dY=(dY, "MN"), dX=(dX, "MK"), dW=(dW, "NK"))
+    if out is None:
+        dX = torch.empty((M, K), dtype=torch.bfloat16, device=X.device) if need_dx else None
+        dW = torch.empty((N, K), dtype=torch.bfloat16, device=X.device) if need_dw else None
+    ws = fp4_workspace(M, N, K, fmt, True, X.device) if ws is None else _req(ws, "ws", torch.uint8)
+    _here(X, codes, scales, tscale, x_tscale, dY, dX, dW, ws)
+    _call("eqat_fp4_linear_bwd", _p(X), _p(codes), _p(scales), f, _p(x_tscale), _p(tscale), _p(dY), _p(dX), _p(dW),
+          M, N, K, _p(ws), ws.numel(), _stream())
+    return dX, dW
 
 
 class AdamwTensor(ctypes.Structure):

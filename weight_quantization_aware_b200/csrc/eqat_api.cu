@@ -15,6 +15,8 @@
 #include "../../include/eqat.h"
 #include "eqat_internal.h"
 
+static_assert(EQAT_TOP_MAX == eqat::kTopMax && EQAT_DISTILL_MAX_V == eqat::kDistillMaxV, "limits of the row kernels");
+
 namespace eqat {
 
 cudaError_t current_device_info(DeviceInfo &info) {
@@ -787,6 +789,250 @@ eqat_status eqat_adamw_step(const eqat_adamw_tensor *tensors, int n_tensors, con
     if (n == 0) return EQAT_OK;
     EQAT_TRY(get_device(dev));
     EQAT_CUDA(eqat::launch_adamw(segs, n, dev, reinterpret_cast<cudaStream_t>(stream)), "adamw");
+    return EQAT_OK;
+}
+
+// ------------------------------------------------------------------ rows of logits
+
+namespace {
+
+// Arrays of the row operators: present where they have elements, aligned to their type.
+eqat_status check_array(const void *p, int64_t elems, uintptr_t align, const char *name) {
+    static thread_local char msg[128];
+    if (elems > 0 && p == nullptr) {
+        std::snprintf(msg, sizeof(msg), "%s is NULL", name);
+        return fail(EQAT_ERR_NULL, msg);
+    }
+    if (p && !aligned(p, align)) {
+        std::snprintf(msg, sizeof(msg), "%s is not %d-byte aligned", name, static_cast<int>(align));
+        return fail(EQAT_ERR_ALIGN, msg);
+    }
+    return EQAT_OK;
+}
+
+eqat_status check_rows(const void *x, int dt, int64_t ld, int64_t T, int64_t V, double temperature) {
+    EQAT_TRY(check_dtype(dt));
+    if (T < 0 || V < 0) return fail(EQAT_ERR_SHAPE, "negative size");
+    const int64_t lim = int64_t(1) << 31;
+    if (T >= lim || V >= lim || ld >= lim) return fail(EQAT_ERR_SHAPE, "a dimension is 2^31 or more");
+    if (T > 0 && V == 0) return fail(EQAT_ERR_SHAPE, "rows without entries");
+    if (ld < V) return fail(EQAT_ERR_SHAPE, "the row stride is smaller than a row");
+    if (!(temperature >= 1e-6 && temperature <= 1e6))
+        return fail(EQAT_ERR_UNSUPPORTED, "temperature must be within 1e-6 .. 1e6");
+    return check_ptr(x, T * V, "x");
+}
+
+// ------------------------------------------------------------------ microscaled 4-bit floats
+
+eqat_status check_fp4(int64_t M, int64_t N, int64_t K, int fmt, const float *gx, const float *gw) {
+    if (fmt != EQAT_FP4_MX && fmt != EQAT_FP4_NV)
+        return fail(EQAT_ERR_UNSUPPORTED, "fmt must be EQAT_FP4_MX or EQAT_FP4_NV");
+    if (M < 0 || N < 0 || K < 0) return fail(EQAT_ERR_SHAPE, "negative size");
+    if (K % 32 != 0) return fail(EQAT_ERR_SHAPE, "K must be a multiple of 32");
+    const int64_t lim = int64_t(1) << 31;
+    if (M >= lim || N >= lim || K >= lim) return fail(EQAT_ERR_SHAPE, "a dimension is 2^31 or more");
+    if (fmt == EQAT_FP4_MX && (gx || gw)) return fail(EQAT_ERR_UNSUPPORTED, "the mx format has no tensor scale");
+    EQAT_TRY(check_array(gx, 0, 4, "tensor scale"));
+    return check_array(gw, 0, 4, "tensor scale");
+}
+
+int64_t fp4_scale_bytes(int64_t N, int64_t K, int fmt) {
+    const int64_t G = K / (fmt == EQAT_FP4_NV ? 16 : 32);
+    return ((N + 127) / 128) * ((G + 3) / 4) * 512;
+}
+
+size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+
+size_t fp4_ws(int64_t M, int64_t N, int64_t K, int fmt, bool backward) {
+    const size_t m = static_cast<size_t>(M), n = static_cast<size_t>(N), k = static_cast<size_t>(K);
+    if (backward) return up256(n * k * 2) + up256(m * k * 2);
+    return up256(m * k / 2) + static_cast<size_t>(fp4_scale_bytes(M, K, fmt));
+}
+
+eqat_status check_fp4_ws(const void *ws, size_t ws_bytes, size_t need) {
+    if (need == 0) return EQAT_OK;
+    if (!ws || ws_bytes < need)
+        return fail(EQAT_ERR_WORKSPACE, "workspace missing or smaller than eqat_fp4_workspace_bytes()");
+    if (!aligned(ws, 256)) return fail(EQAT_ERR_ALIGN, "workspace is not 256-byte aligned");
+    return EQAT_OK;
+}
+
+}  // namespace
+
+eqat_status eqat_token_logprobs(const void *x, int dt, int64_t ld, int64_t T, int64_t V, const int64_t *targets,
+                                double temperature, int top_k, float *logprob, float *entropy, int64_t *top_ids,
+                                float *top_logprobs, eqat_stream_t stream) {
+    DeviceInfo dev;
+    EQAT_TRY(check_rows(x, dt, ld, T, V, temperature));
+    if (top_k < 0 || top_k > EQAT_TOP_MAX) return fail(EQAT_ERR_UNSUPPORTED, "top_k must be 0..EQAT_TOP_MAX");
+    EQAT_TRY(check_array(targets, T, 8, "targets"));
+    EQAT_TRY(check_array(logprob, T, 4, "logprob"));
+    EQAT_TRY(check_array(entropy, T, 4, "entropy"));
+    EQAT_TRY(check_array(top_ids, T * top_k, 8, "top_ids"));
+    EQAT_TRY(check_array(top_logprobs, T * top_k, 4, "top_logprobs"));
+    if (T == 0) return EQAT_OK;
+    EQAT_TRY(get_device(dev));
+    EQAT_CUDA(eqat::launch_token_logprobs(x, dt == EQAT_F32, ld, T, V, targets, temperature, top_k, logprob, entropy,
+                                          top_ids, top_logprobs, dev, reinterpret_cast<cudaStream_t>(stream)),
+              "token_logprobs");
+    return EQAT_OK;
+}
+
+eqat_status eqat_distill_topk(const void *x, int dt, int64_t ld, int64_t T, int64_t V, const int64_t *ids,
+                              const float *tlp, int k, double temperature, uint32_t flags, const float *weight,
+                              float *loss, void *dx, eqat_stream_t stream) {
+    DeviceInfo dev;
+    EQAT_TRY(check_rows(x, dt, ld, T, V, temperature));
+    if (V > EQAT_DISTILL_MAX_V) return fail(EQAT_ERR_SHAPE, "V is above EQAT_DISTILL_MAX_V");
+    if (k < 1 || k > EQAT_TOP_MAX) return fail(EQAT_ERR_UNSUPPORTED, "k must be 1..EQAT_TOP_MAX");
+    if (flags & ~EQAT_DISTILL_TAIL) return fail(EQAT_ERR_UNSUPPORTED, "unknown flag bits");
+    EQAT_TRY(check_array(ids, T * k, 8, "ids"));
+    EQAT_TRY(check_array(tlp, T * k, 4, "tlp"));
+    EQAT_TRY(check_array(weight, 0, 4, "weight"));
+    EQAT_TRY(check_array(loss, 0, 4, "loss"));
+    EQAT_TRY(check_ptr(dx, 0, "dx"));
+    if (T == 0 || (!loss && !dx)) return EQAT_OK;
+    EQAT_TRY(get_device(dev));
+    EQAT_CUDA(eqat::launch_distill_topk(x, dt == EQAT_F32, ld, T, V, ids, tlp, k, temperature,
+                                        (flags & EQAT_DISTILL_TAIL) != 0, weight, loss, dx, dev,
+                                        reinterpret_cast<cudaStream_t>(stream)),
+              "distill_topk");
+    return EQAT_OK;
+}
+
+size_t eqat_fp4_scale_bytes(int64_t N, int64_t K, int fmt) {
+    if (check_fp4(0, N, K, fmt, nullptr, nullptr) != EQAT_OK) return 0;
+    return static_cast<size_t>(fp4_scale_bytes(N, K, fmt));
+}
+
+size_t eqat_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int backward) {
+    if (check_fp4(M, N, K, fmt, nullptr, nullptr) != EQAT_OK) return 0;
+    return fp4_ws(M, N, K, fmt, backward != 0);
+}
+
+eqat_status eqat_fp4_tensor_scale(const void *x, int dt, int64_t n, float *g, eqat_stream_t stream) {
+    DeviceInfo dev;
+    EQAT_TRY(check_dtype(dt));
+    if (n < 0 || n % 32 != 0) return fail(EQAT_ERR_SHAPE, "n must be a multiple of 32");
+    EQAT_TRY(check_ptr(x, n, "x"));
+    EQAT_TRY(check_array(g, 1, 4, "g"));
+    EQAT_TRY(get_device(dev));
+    EQAT_CUDA(eqat::launch_tensor_scale_fp4(x, dt == EQAT_F32, n, g, dev, reinterpret_cast<cudaStream_t>(stream)),
+              "fp4 tensor scale");
+    return EQAT_OK;
+}
+
+eqat_status eqat_pack_fp4(const void *x, int dt, int64_t N, int64_t K, int fmt, const float *g, uint8_t *codes,
+                          uint8_t *scales, eqat_stream_t stream) {
+    DeviceInfo dev;
+    EQAT_TRY(check_dtype(dt));
+    EQAT_TRY(check_fp4(0, N, K, fmt, g, nullptr));
+    EQAT_TRY(check_ptr(x, N * K, "x"));
+    EQAT_TRY(check_ptr(codes, N * K, "codes"));
+    EQAT_TRY(check_ptr(scales, N * K, "scales"));
+    if (N * K == 0) return EQAT_OK;
+    EQAT_TRY(get_device(dev));
+    EQAT_CUDA(eqat::launch_encode_fp4(x, dt == EQAT_F32, fmt == EQAT_FP4_NV, g, N, K, codes, scales, nullptr, dev,
+                                      reinterpret_cast<cudaStream_t>(stream)),
+              "pack_fp4");
+    return EQAT_OK;
+}
+
+eqat_status eqat_fake_quant_fp4(const void *x, int dt, int64_t N, int64_t K, int fmt, const float *g, void *x_hat,
+                                eqat_stream_t stream) {
+    DeviceInfo dev;
+    EQAT_TRY(check_dtype(dt));
+    EQAT_TRY(check_fp4(0, N, K, fmt, g, nullptr));
+    EQAT_TRY(check_ptr(x, N * K, "x"));
+    EQAT_TRY(check_ptr(x_hat, N * K, "x_hat"));
+    if (N * K == 0) return EQAT_OK;
+    EQAT_TRY(get_device(dev));
+    EQAT_CUDA(eqat::launch_encode_fp4(x, dt == EQAT_F32, fmt == EQAT_FP4_NV, g, N, K, nullptr, nullptr, x_hat, dev,
+                                      reinterpret_cast<cudaStream_t>(stream)),
+              "fake_quant_fp4");
+    return EQAT_OK;
+}
+
+eqat_status eqat_dequant_fp4(const uint8_t *codes, const uint8_t *scales, int64_t N, int64_t K, int fmt,
+                             const float *g, void *values, int dt, eqat_stream_t stream) {
+    DeviceInfo dev;
+    EQAT_TRY(check_dtype(dt));
+    EQAT_TRY(check_fp4(0, N, K, fmt, g, nullptr));
+    EQAT_TRY(check_ptr(codes, N * K, "codes"));
+    EQAT_TRY(check_ptr(scales, N * K, "scales"));
+    EQAT_TRY(check_ptr(values, N * K, "values"));
+    if (N * K == 0) return EQAT_OK;
+    EQAT_TRY(get_device(dev));
+    EQAT_CUDA(eqat::launch_dequant_fp4(codes, scales, fmt == EQAT_FP4_NV, g, N, K, values, dt == EQAT_F32, dev,
+                                       reinterpret_cast<cudaStream_t>(stream)),
+              "dequant_fp4");
+    return EQAT_OK;
+}
+
+eqat_status eqat_fp4_linear_fwd(const void *X, const uint8_t *codes, const uint8_t *scales, int fmt,
+                                const float *gx, const float *gw, void *Y, int64_t M, int64_t N, int64_t K,
+                                void *ws, size_t ws_bytes, eqat_stream_t stream) {
+    DeviceInfo dev;
+    EQAT_TRY(check_fp4(M, N, K, fmt, gx, gw));
+    if (N % 8 != 0) return fail(EQAT_ERR_SHAPE, "N must be a multiple of 8");
+    EQAT_TRY(check_ptr(X, M * K, "X"));
+    EQAT_TRY(check_ptr(codes, N * K, "codes"));
+    EQAT_TRY(check_ptr(scales, N * K, "scales"));
+    EQAT_TRY(check_ptr(Y, M * N, "Y"));
+    if (M * N == 0) return EQAT_OK;
+    if (K > 0) EQAT_TRY(check_fp4_ws(ws, ws_bytes, fp4_ws(M, N, K, fmt, false)));
+    EQAT_TRY(get_device(dev));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (K == 0) {
+        EQAT_CUDA(zero(Y, static_cast<size_t>(M * N) * 2, st), "memset Y");
+        return EQAT_OK;
+    }
+    const bool nv = fmt == EQAT_FP4_NV;
+    uint8_t *xc = static_cast<uint8_t *>(ws), *xs = xc + up256(static_cast<size_t>(M * K) / 2);
+    EQAT_CUDA(eqat::launch_encode_fp4(X, false, nv, gx, M, K, xc, xs, nullptr, dev, st), "fp4 pack of X");
+    EQAT_CUDA(eqat::launch_gemm_fp4(xc, xs, gx, codes, scales, gw, nv, M, N, K, Y, dev, st), "fp4 product");
+    return EQAT_OK;
+}
+
+eqat_status eqat_fp4_linear_bwd(const void *X, const uint8_t *codes, const uint8_t *scales, int fmt,
+                                const float *gx, const float *gw, const void *dY, void *dX, void *dW, int64_t M,
+                                int64_t N, int64_t K, void *ws, size_t ws_bytes, eqat_stream_t stream) {
+    DeviceInfo dev;
+    EQAT_TRY(check_fp4(M, N, K, fmt, gx, gw));
+    if (N % 8 != 0) return fail(EQAT_ERR_SHAPE, "N must be a multiple of 8");
+    EQAT_TRY(check_ptr(X, M * K, "X"));
+    EQAT_TRY(check_ptr(codes, N * K, "codes"));
+    EQAT_TRY(check_ptr(scales, N * K, "scales"));
+    EQAT_TRY(check_ptr(dY, M * N, "dY"));
+    EQAT_TRY(check_ptr(dX, 0, "dX"));
+    EQAT_TRY(check_ptr(dW, 0, "dW"));
+    if ((!dX && !dW) || K == 0) return EQAT_OK;
+    if (M * N > 0) EQAT_TRY(check_fp4_ws(ws, ws_bytes, fp4_ws(M, N, K, fmt, true)));
+    EQAT_TRY(get_device(dev));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    if (M * N == 0) {  // empty sums
+        EQAT_CUDA(zero(dX, static_cast<size_t>(M * K) * 2, st), "memset dX");
+        EQAT_CUDA(zero(dW, static_cast<size_t>(N * K) * 2, st), "memset dW");
+        return EQAT_OK;
+    }
+    const bool nv = fmt == EQAT_FP4_NV;
+    uint8_t *w_hat = static_cast<uint8_t *>(ws), *x_hat = w_hat + up256(static_cast<size_t>(N * K) * 2);
+    EpiArgs epi;
+    epi.kind = Epi::kStore;
+    epi.ldo = K;
+    if (dX) {
+        EQAT_CUDA(eqat::launch_dequant_fp4(codes, scales, nv, gw, N, K, w_hat, false, dev, st), "fp4 values of W");
+        epi.out = dX;
+        EQAT_CUDA(eqat::launch_gemm_tc(Operand{dY, N, false}, Operand{w_hat, K, true}, M, K, N, epi, dev, st),
+                  "fp4 input gradient");
+    }
+    if (dW) {
+        EQAT_CUDA(eqat::launch_encode_fp4(X, false, nv, gx, M, K, nullptr, nullptr, x_hat, dev, st),
+                  "fp4 values of X");
+        epi.out = dW;
+        EQAT_CUDA(eqat::launch_gemm_tc(Operand{dY, N, true}, Operand{x_hat, K, true}, N, K, M, epi, dev, st),
+                  "fp4 weight gradient");
+    }
     return EQAT_OK;
 }
 

@@ -1,0 +1,371 @@
+// Products of microscaled 4-bit matrices on sm_100a tensor cores: D = A B^T with A and B
+// K-major e2m1 codes, a scale for each block of 16 (e4m3) or 32 (e8m0) of K on both
+// sides, fp32 accumulation in tensor memory (tcgen05.mma, block-scaled kinds).
+//
+// Y[M, N] = X W^T runs with the tokens as the 128 rows of a tile, or, for few tokens,
+// with the weights as the rows (SWAP): the tile is then as narrow as the tokens, and the
+// call streams the weights once.
+//
+// A CTA makes one 128 x NT tile.  A producer thread brings stages of 256 K values: the
+// code tiles by TMA (128 bytes of K per row, 128-byte swizzle) and the scale tiles by
+// bulk copies.  The issuing thread copies a stage's scale tiles from shared to tensor
+// memory (tcgen05.cp, ordered before the MMAs that read them) and issues one MMA per 64
+// values of K.  Each ring slot has its own scale columns in tensor memory, so that the
+// barrier that frees the slot's shared memory frees them too.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cstdint>
+
+#include "eqat_internal.h"
+#include "eqat_pdl.cuh"
+#include "eqat_ptx.cuh"
+#include "eqat_qmath.cuh"
+
+namespace eqat {
+namespace {
+
+constexpr uint64_t kWaitLimitNs = 4000000000ull;
+constexpr int kKStage = 256;         // K values per stage: 128 bytes of codes per row
+constexpr int kSfTile = 512;         // bytes of a scale tile: 128 rows x 4 blocks
+constexpr int kATile = 128 * 128;    // bytes of A per stage
+constexpr int kThreads = 192;        // producer, issuer, four epilogue warps
+
+template <int NT, bool NV>
+struct Cfg {
+    static constexpr int SF = NV ? 4 : 2;              // scale tiles of a stage per 128 rows
+    static constexpr int KSF = NV ? 64 : 128;          // K values of a scale tile
+    static constexpr int RB = NT > 128 ? 2 : 1;        // 128-row scale tiles of B
+    static constexpr int BTILE = NT * 128;
+    static constexpr int STAGE = kATile + BTILE + SF * kSfTile * (1 + RB);
+    static constexpr int STAGES = NT >= 256 ? 4 : NT >= 128 ? 6 : NT >= 64 ? 7 : 8;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + 256;
+    static constexpr int ACC = NT < 32 ? 32 : NT;      // accumulator columns
+    static constexpr int SF_COLS = SF * 4 * (1 + RB);  // scale columns of a stage
+    static_assert(ACC + STAGES * SF_COLS <= 512, "tensor memory columns");
+    static_assert(SMEM <= 232448, "shared memory");
+    static_assert(STAGE % 1024 == 0, "swizzled tiles start on 1024 bytes");
+};
+
+struct Ctl {
+    uint64_t full[8], empty[8], acc_full, drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(Ctl) <= 256, "control block exceeds its slot");
+
+struct Args {
+    const uint8_t *sfa, *sfb;   // scale tiles
+    int64_t sf_tiles_k;         // scale tiles along K (the same on both sides)
+    int64_t rows_a, rows_b;     // rows of A and B
+    int K;
+    const float *ga, *gb;       // tensor scales (nullable)
+    __nv_bfloat16 *Y;
+    int64_t ldy;
+    int tiles_a;
+    int *err;
+    uint64_t wait_limit_ns;
+};
+
+__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// Copies one scale tile (32 rows of 16 bytes) to four tensor-memory columns, repeated in
+// each of the four lane quadrants.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Unswizzled shared-memory descriptor; 8-row groups of 16-byte rows are 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
+    d |= static_cast<uint64_t>(128 >> 4) << 16;
+    d |= static_cast<uint64_t>(128 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    return d;
+}
+
+// Instruction descriptor of the block-scaled e2m1 kinds, K-major operands, M = 128;
+// sf_id: the first scale of the 32-bit scale cells that this instruction reads.
+__device__ constexpr uint32_t idesc_fp4(int n, bool nv, uint32_t sf_id) {
+    return (sf_id << 4)                          // B scale id
+           | (1u << 7)                           // A format: e2m1
+           | (1u << 10)                          // B format: e2m1
+           | (static_cast<uint32_t>(n >> 3) << 17)
+           | (nv ? 0u : (1u << 23))              // scale format: e4m3 or e8m0
+           | (1u << 27)                          // M / 128
+           | (sf_id << 29);                      // A scale id
+}
+
+template <bool NV>
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate) {
+    if (NV)
+        asm volatile(
+            "{\n"
+            ".reg .pred p;\n"
+            "setp.ne.b32 p, %6, 0;\n"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n"
+            "}\n" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n"
+            ".reg .pred p;\n"
+            "setp.ne.b32 p, %6, 0;\n"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n"
+            "}\n" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, float (&v)[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+template <int NT, bool NV, bool SWAP>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_gemm_fp4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Args p) {
+    using C = Cfg<NT, NV>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + C::STAGES * C::STAGE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&ctl->full[i], 1);
+            mbar_init(&ctl->empty[i], 1);
+        }
+        mbar_init(&ctl->acc_full, 1);
+        mbar_init(&ctl->drain, 1);
+        ctl->abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_allow_dependents();
+    if (warp == 2) {
+        tmem_alloc(&ctl->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    volatile int *abort_flag = &ctl->abort_flag;
+    const int ta = blockIdx.x % p.tiles_a, tb = blockIdx.x / p.tiles_a;
+    const int nkb = (p.K + kKStage - 1) / kKStage;
+
+    if (warp == 0) {
+        if (elect_one_sync()) {
+            uint32_t armed = 0, armed_parity = 0;
+            bool ok = true;
+            // scale tiles of B that exist (its rows past the last tile of 128 have none)
+            const int rb = C::RB == 1 || static_cast<int64_t>(tb) * NT + 128 < p.rows_b ? C::RB : 1;
+            const int64_t b_rowtile = static_cast<int64_t>(tb) * NT / 128;
+            for (int kb = 0; kb < nkb; ++kb) {
+                const int st = kb % C::STAGES;
+                const uint32_t ph = (kb / C::STAGES) & 1u;
+                if (!mbar_wait_bounded(&ctl->empty[st], ph ^ 1u, abort_flag, p.err, p.wait_limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *sa = smem + st * C::STAGE, *sb = sa + kATile, *sfa = sb + C::BTILE,
+                        *sfb = sfa + C::SF * kSfTile;
+                const int64_t sf0 = static_cast<int64_t>(kb) * C::SF;
+                const int64_t left = p.sf_tiles_k - sf0;
+                const uint32_t sf_bytes = static_cast<uint32_t>(left < C::SF ? left : C::SF) * kSfTile;
+                mbar_arrive_expect_tx(&ctl->full[st], kATile + C::BTILE + sf_bytes * (1 + rb));
+                armed |= 1u << st;
+                armed_parity = (armed_parity & ~(1u << st)) | (ph << st);
+                tma_load_2d(sa, &tmA, &ctl->full[st], kb * 128, ta * 128);
+                tma_load_2d(sb, &tmB, &ctl->full[st], kb * 128, tb * NT);
+                bulk_load(sfa, p.sfa + (ta * p.sf_tiles_k + sf0) * kSfTile, sf_bytes, &ctl->full[st]);
+                for (int h = 0; h < rb; ++h)
+                    bulk_load(sfb + h * C::SF * kSfTile, p.sfb + ((b_rowtile + h) * p.sf_tiles_k + sf0) * kSfTile,
+                              sf_bytes, &ctl->full[st]);
+            }
+            if (!ok) {  // let the copies already issued land before the block exits
+                for (int st = 0; st < C::STAGES; ++st)
+                    if (armed & (1u << st)) {
+                        const uint32_t a = smem_u32(&ctl->full[st]);
+                        const uint64_t t0 = globaltimer_ns();
+                        while (!mbar_try_wait(a, (armed_parity >> st) & 1u) && globaltimer_ns() - t0 < 100000000ull) {
+                        }
+                    }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (elect_one_sync()) {
+            bool ok = true;
+            for (int kb = 0; kb < nkb; ++kb) {
+                const int st = kb % C::STAGES;
+                const uint32_t ph = (kb / C::STAGES) & 1u;
+                if (!mbar_wait_bounded(&ctl->full[st], ph, abort_flag, p.err, p.wait_limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sa = smem_u32(smem + st * C::STAGE), sb = sa + kATile, ssfa = sb + C::BTILE,
+                               ssfb = ssfa + C::SF * kSfTile;
+                // A's scales, then B's, of each scale tile of the stage
+                const uint32_t tsf = tmem + C::ACC + st * C::SF_COLS;
+                const int kleft = p.K - kb * kKStage;
+                const int nsf = kleft >= kKStage ? C::SF : (kleft + C::KSF - 1) / C::KSF;
+                for (int j = 0; j < nsf; ++j) {
+                    tmem_cp_scales(tsf + j * 4, smem_desc_plain(ssfa + j * kSfTile));
+#pragma unroll
+                    for (int h = 0; h < C::RB; ++h)
+                        tmem_cp_scales(tsf + C::SF * 4 + (j * C::RB + h) * 4,
+                                       smem_desc_plain(ssfb + (h * C::SF + j) * kSfTile));
+                }
+                const int nmma = kleft >= kKStage ? kKStage / 64 : (kleft + 63) / 64;
+                for (int kk = 0; kk < nmma; ++kk) {
+                    const uint64_t ad = smem_desc_sw128(sa + kk * 32, 16, 1024);
+                    const uint64_t bd = smem_desc_sw128(sb + kk * 32, 16, 1024);
+                    const int j = NV ? kk : kk >> 1;
+                    const uint32_t id = NV ? 0u : (kk & 1) * 2u;
+                    mma_fp4<NV>(tmem, ad, bd, idesc_fp4(NT, NV, id), tsf + j * 4, tsf + C::SF * 4 + j * C::RB * 4,
+                                (kb > 0 || kk > 0) ? 1u : 0u);
+                }
+                tc_commit(&ctl->empty[st]);
+            }
+            if (ok) {
+                tc_commit(&ctl->acc_full);
+            } else {  // wait for the MMAs already issued before tensor memory is freed
+                tc_commit(&ctl->drain);
+                const uint32_t a = smem_u32(&ctl->drain);
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < 100000000ull) {
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        const int quad = warp & 3;
+        const float alpha = (p.ga ? __ldg(p.ga) : 1.0f) * (p.gb ? __ldg(p.gb) : 1.0f);
+        const bool ok = mbar_wait_bounded(&ctl->acc_full, 0, abort_flag, p.err, p.wait_limit_ns);
+        if (__all_sync(0xffffffffu, ok)) {
+            tc_fence_after();
+            const int64_t row = static_cast<int64_t>(ta) * 128 + quad * 32 + lane;
+            const uint32_t taddr = tmem + ((quad * 32) << 16);
+#pragma unroll 1
+            for (int c0 = 0; c0 < NT; c0 += 16) {
+                float v[16];
+                tmem_ld_16cols(taddr + c0, v);
+                const int64_t col = static_cast<int64_t>(tb) * NT + c0;
+                if (row >= p.rows_a) continue;
+                if (SWAP) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (col + j < p.rows_b)
+                            p.Y[(col + j) * p.ldy + row] = __float2bfloat16_rn(__fmul_rn(v[j], alpha));
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)  // rows of Y are multiples of 8 values
+                        if (col + 8 * q < p.rows_b) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                w[j] = pack_bf16x2(__fmul_rn(v[8 * q + 2 * j], alpha),
+                                                   __fmul_rn(v[8 * q + 2 * j + 1], alpha));
+                            *reinterpret_cast<uint4 *>(p.Y + row * p.ldy + col + 8 * q) =
+                                make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+struct Side {
+    const uint8_t *codes, *scales;
+    const float *g;
+    int64_t rows;
+};
+
+template <int NT, bool NV, bool SWAP>
+cudaError_t launch_t(const Side &a, const Side &b, int64_t K, void *Y, int64_t ldy, const DeviceInfo &dev,
+                     cudaStream_t st) {
+    using C = Cfg<NT, NV>;
+    CUtensorMap ma, mb;
+    cudaError_t e = encode_map_2d(ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, K / 2, a.rows, K / 2, 128, 128,
+                                  CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    e = encode_map_2d(mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, b.codes, K / 2, b.rows, K / 2, 128, NT,
+                      CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    auto kern = k_gemm_fp4<NT, NV, SWAP>;
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << (dev.device & 63);
+    if (!(done.load() & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit);
+    }
+    Args p{};
+    p.sfa = a.scales;
+    p.sfb = b.scales;
+    p.sf_tiles_k = (K / (NV ? 16 : 32) + 3) / 4;
+    p.rows_a = a.rows;
+    p.rows_b = b.rows;
+    p.K = static_cast<int>(K);
+    p.ga = a.g;
+    p.gb = b.g;
+    p.Y = static_cast<__nv_bfloat16 *>(Y);
+    p.ldy = ldy;
+    p.tiles_a = static_cast<int>((a.rows + 127) / 128);
+    p.err = device_error_word();
+    if (!p.err) return cudaErrorInvalidSymbol;
+    p.wait_limit_ns = kWaitLimitNs;
+    const int64_t tiles = static_cast<int64_t>(p.tiles_a) * ((b.rows + NT - 1) / NT);
+    if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), C::SMEM, st, ma, mb, p);
+}
+
+template <bool NV>
+cudaError_t dispatch(const Side &x, const Side &w, int64_t K, void *Y, const DeviceInfo &dev, cudaStream_t st) {
+    const int64_t M = x.rows, N = w.rows;
+    if (M <= 16) return launch_t<16, NV, true>(w, x, K, Y, N, dev, st);
+    if (M <= 32) return launch_t<32, NV, true>(w, x, K, Y, N, dev, st);
+    if (M <= 64) return launch_t<64, NV, true>(w, x, K, Y, N, dev, st);
+    if (M <= 128) return launch_t<128, NV, true>(w, x, K, Y, N, dev, st);
+    return launch_t<256, NV, false>(x, w, K, Y, N, dev, st);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm_fp4(const uint8_t *x_codes, const uint8_t *x_scales, const float *gx, const uint8_t *w_codes,
+                            const uint8_t *w_scales, const float *gw, bool nv, int64_t M, int64_t N, int64_t K,
+                            void *Y, const DeviceInfo &dev, cudaStream_t st) {
+    const Side x{x_codes, x_scales, gx, M}, w{w_codes, w_scales, gw, N};
+    return nv ? dispatch<true>(x, w, K, Y, dev, st) : dispatch<false>(x, w, K, Y, dev, st);
+}
+
+}  // namespace eqat

@@ -179,6 +179,32 @@ cudaError_t launch_mse_f32(float *dY, const float *target, int64_t n, float scal
 cudaError_t launch_mse_zero_bf16(void *dY, const void *target, int64_t n, float scale, double *loss,
                                  const DeviceInfo &dev, cudaStream_t st);
 
+// ------------------------------------------------------------------ rows of logits
+// x [T, V] bf16 or fp32, row stride ld elements.
+constexpr int kTopMax = 128;                   // alternatives per row
+constexpr int64_t kDistillMaxV = int64_t(1) << 20;  // a bit per vocabulary entry in shared memory
+cudaError_t launch_token_logprobs(const void *x, bool f32, int64_t ld, int64_t T, int64_t V, const int64_t *targets,
+                                  double temperature, int k, float *logprob, float *entropy, int64_t *top_ids,
+                                  float *top_logprobs, const DeviceInfo &dev, cudaStream_t st);
+// dx (row stride ld, nullable) may be x; loss and weight are nullable.
+cudaError_t launch_distill_topk(const void *x, bool f32, int64_t ld, int64_t T, int64_t V, const int64_t *ids,
+                                const float *tlp, int k, double temperature, bool tail, const float *weight,
+                                float *loss, void *dx, const DeviceInfo &dev, cudaStream_t st);
+
+// ------------------------------------------------------------------ microscaled 4-bit floats
+// x [N, K] -> codes [N, K / 2], scale tiles, values [N, K] (each nullable; codes and
+// scales together); g: tensor scale of the nv format (nullable: 1).
+cudaError_t launch_encode_fp4(const void *x, bool f32, bool nv, const float *g, int64_t N, int64_t K, uint8_t *codes,
+                              uint8_t *scales, void *values, const DeviceInfo &dev, cudaStream_t st);
+cudaError_t launch_dequant_fp4(const uint8_t *codes, const uint8_t *scales, bool nv, const float *g, int64_t N,
+                               int64_t K, void *out, bool f32, const DeviceInfo &dev, cudaStream_t st);
+cudaError_t launch_tensor_scale_fp4(const void *x, bool f32, int64_t n, float *out, const DeviceInfo &dev,
+                                    cudaStream_t st);
+// Y[M, N] (bf16) = X W^T, both sides packed.
+cudaError_t launch_gemm_fp4(const uint8_t *x_codes, const uint8_t *x_scales, const float *gx, const uint8_t *w_codes,
+                            const uint8_t *w_scales, const float *gw, bool nv, int64_t M, int64_t N, int64_t K,
+                            void *Y, const DeviceInfo &dev, cudaStream_t st);
+
 // Records the message that eqat_last_error_detail() returns on this thread.
 void set_error_detail(const char *msg);
 
