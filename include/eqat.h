@@ -323,7 +323,7 @@ eqat_status eqat_fq_linear_fwd_noalloc(const void *X, const void *W, int dt, con
  * written.  x is 16-byte aligned; the other arrays need their element's alignment
  * only (a shifted view of the labels is fine).  temperature is within 1e-6 .. 1e6 and
  * divides the logits; an entry of -inf is masked: it has no probability and is never
- * an alternative.  V < 2^31.
+ * an alternative.  V <= 2^30; T, ld < 2^31.
  *
  * eqat_token_logprobs: with lse the log of sum exp(x / temperature) over a row,
  *   logprob[t] = x[t, targets[t]] / temperature - lse      0 where targets[t] < 0,
@@ -360,7 +360,7 @@ eqat_status eqat_token_logprobs(const void *x, int dt, int64_t ld, int64_t T, in
  * slots' masses together.  An id >= V, NaN or +inf in the row, or NaN or +inf in
  * tlp, makes the row's loss and gradient NaN.  V <= EQAT_DISTILL_MAX_V. */
 #define EQAT_DISTILL_TAIL 1u
-#define EQAT_DISTILL_MAX_V 1048576
+#define EQAT_DISTILL_MAX_V 524288
 eqat_status eqat_distill_topk(const void *x, int dt, int64_t ld, int64_t T, int64_t V, const int64_t *ids,
                               const float *tlp, int k, double temperature, uint32_t flags, const float *weight,
                               float *loss, void *dx, eqat_stream_t stream);

@@ -814,7 +814,8 @@ eqat_status check_rows(const void *x, int dt, int64_t ld, int64_t T, int64_t V, 
     EQAT_TRY(check_dtype(dt));
     if (T < 0 || V < 0) return fail(EQAT_ERR_SHAPE, "negative size");
     const int64_t lim = int64_t(1) << 31;
-    if (T >= lim || V >= lim || ld >= lim) return fail(EQAT_ERR_SHAPE, "a dimension is 2^31 or more");
+    if (T >= lim || ld >= lim) return fail(EQAT_ERR_SHAPE, "a dimension is 2^31 or more");
+    if (V > (int64_t(1) << 30)) return fail(EQAT_ERR_SHAPE, "V is above 2^30");
     if (T > 0 && V == 0) return fail(EQAT_ERR_SHAPE, "rows without entries");
     if (ld < V) return fail(EQAT_ERR_SHAPE, "the row stride is smaller than a row");
     if (!(temperature >= 1e-6 && temperature <= 1e6))

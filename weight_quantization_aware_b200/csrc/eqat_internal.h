@@ -182,7 +182,7 @@ cudaError_t launch_mse_zero_bf16(void *dY, const void *target, int64_t n, float 
 // ------------------------------------------------------------------ rows of logits
 // x [T, V] bf16 or fp32, row stride ld elements.
 constexpr int kTopMax = 128;                   // alternatives per row
-constexpr int64_t kDistillMaxV = int64_t(1) << 20;  // a bit per vocabulary entry in shared memory
+constexpr int64_t kDistillMaxV = int64_t(1) << 19;  // two bits per vocabulary entry in shared memory
 cudaError_t launch_token_logprobs(const void *x, bool f32, int64_t ld, int64_t T, int64_t V, const int64_t *targets,
                                   double temperature, int k, float *logprob, float *entropy, int64_t *top_ids,
                                   float *top_logprobs, const DeviceInfo &dev, cudaStream_t st);

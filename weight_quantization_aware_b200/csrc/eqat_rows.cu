@@ -5,10 +5,16 @@
 // Both are HBM-bound: a row is read once from memory, and the gradient written once.
 // A CTA owns a row and walks it in 16-byte vectors.  The first walk keeps a running
 // maximum m, S = sum 2^y and (for the entropy) A = sum 2^y y per thread, with
-// y = (x - m) c and c = log2(e) / temperature; x - m is formed before the product, so
-// that a row masked with the type's lowest value, and the largest entries of any row,
-// lose nothing.  The second walk (top alternatives, gradient) reads the row again
-// while it is in L2.
+// y = (x - m) c and c = log2(e) / temperature.  y is one fma, x c - RN(m c), and what
+// the rounding of m c moved all of a thread's terms by is taken out of S and A at the
+// end (m c - RN(m c) is exact in one fma).  That form needs |x| c far below the fp32
+// range: it starts from m = -1e30, and a row whose S then is 0 or not finite (all
+// entries masked, or at the type's lowest value, or a NaN, an infinity, a value near
+// the type's largest) is walked again with x - m formed first.  The second walk (top
+// alternatives, gradient) reads the row again while it is in L2.
+//
+// What bounds the first walk besides memory is ex2 (a quarter of the issue rate), then
+// instruction issue: one packed-fp32 instruction does two entries of each step.
 //
 // All sums are fp32 per thread (a few hundred terms of one sign), joined over the
 // block in a fixed order; the few values per row (log S, the loss) are fp64.
@@ -16,21 +22,31 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "eqat_internal.h"
 #include "eqat_pdl.cuh"
+#include "eqat_ptx.cuh"
 #include "eqat_qmath.cuh"
 
 namespace eqat {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;  // threads that walk a row
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;         // 16-byte vectors in flight per thread
-constexpr int kCandidates = 2048;  // shared-memory candidates of the top-k selection
+constexpr int kUnroll = 4;                           // 16-byte vectors per thread and chunk
+constexpr int kChunk = kThreads * kUnroll;           // vectors of a chunk: 16 KB
+constexpr int kStages = 3;                           // chunks of the ring
+constexpr size_t kRingBytes = static_cast<size_t>(kStages) * kChunk * 16;
+constexpr int kCtasPerSm = 3;
+constexpr uint64_t kWaitLimitNs = 4000000000ull;     // far above any legitimate wait
+constexpr int kCandidates = 2048;  // vectors with candidates of the top-k selection, in shared memory
+constexpr int kKept = 1024;        // entries among them that are ranked
+constexpr float kFloor = -1e30f;   // below every logit that has a part in its row
 constexpr uint32_t kNegInfBf16x2 = 0xFF80FF80u;
 constexpr uint32_t kNegInfF32 = 0xFF800000u;
 
@@ -89,22 +105,38 @@ struct Vec<__nv_bfloat16> {
         const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
         return fmaxf(__low2float(m), __high2float(m));
     }
-    static __device__ __forceinline__ void set(uint4 &r, int j, uint32_t raw) {
-        uint32_t *w = reinterpret_cast<uint32_t *>(&r);
-        const int sh = 16 * (j & 1);
+    template <int U>
+    static __device__ __forceinline__ float max(const uint4 (&r)[U]) {
+        __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162 *>(&r[0]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i == (j >> 1)) w[i] = (w[i] & ~(0xFFFFu << sh)) | ((raw & 0xFFFFu) << sh);
+        for (int u = 0; u < U; ++u) {
+            const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&r[u]);
+            m = __hmax2(m, __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+        }
+        return fmaxf(__low2float(m), __high2float(m));
+    }
+    // entries below kFloor (masked ones) to about kFloor; NaN stays
+    static __device__ __forceinline__ uint4 clamp(uint4 r) {
+        __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&r);
+        const __nv_bfloat162 f = __float2bfloat162_rn(kFloor);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __hmax2_nan(h[i], f);
+        return r;
+    }
+    static __device__ __forceinline__ void set(uint4 &r, int j, uint32_t raw) {
+        const int sh = 16 * (j & 1), i = j >> 1;
+        const uint32_t keep = ~(0xFFFFu << sh), put = (raw & 0xFFFFu) << sh;
+        r.x = i == 0 ? (r.x & keep) | put : r.x;
+        r.y = i == 1 ? (r.y & keep) | put : r.y;
+        r.z = i == 2 ? (r.z & keep) | put : r.z;
+        r.w = i == 3 ? (r.w & keep) | put : r.w;
     }
     static __device__ __forceinline__ uint32_t raw(const __nv_bfloat16 *p) {
         return *reinterpret_cast<const unsigned short *>(p);
     }
     static __device__ __forceinline__ float value(const uint4 &r, int j) {
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(&r);
-        uint32_t x = w[0];
-#pragma unroll
-        for (int i = 1; i < 4; ++i)
-            if (i == (j >> 1)) x = w[i];
+        const int i = j >> 1;
+        const uint32_t x = i == 0 ? r.x : i == 1 ? r.y : i == 2 ? r.z : r.w;
         return (j & 1) ? bf16_hi(x) : bf16_lo(x);
     }
     static __device__ __forceinline__ uint4 from_pairs(const uint64_t (&p)[4]) {
@@ -133,20 +165,28 @@ struct Vec<float> {
                            fmaxf(__uint_as_float(r.z), __uint_as_float(r.w))),
                      -INFINITY);
     }
-    static __device__ __forceinline__ void set(uint4 &r, int j, uint32_t raw) {
+    template <int U>
+    static __device__ __forceinline__ float max(const uint4 (&r)[U]) {
+        float m = max(r[0]);
+#pragma unroll
+        for (int u = 1; u < U; ++u) m = fmaxf(m, max(r[u]));
+        return m;
+    }
+    static __device__ __forceinline__ uint4 clamp(uint4 r) {
         uint32_t *w = reinterpret_cast<uint32_t *>(&r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i == j) w[i] = raw;
+        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(max_nan(__uint_as_float(w[i]), kFloor));
+        return r;
+    }
+    static __device__ __forceinline__ void set(uint4 &r, int j, uint32_t raw) {
+        r.x = j == 0 ? raw : r.x;
+        r.y = j == 1 ? raw : r.y;
+        r.z = j == 2 ? raw : r.z;
+        r.w = j == 3 ? raw : r.w;
     }
     static __device__ __forceinline__ uint32_t raw(const float *p) { return __float_as_uint(*p); }
     static __device__ __forceinline__ float value(const uint4 &r, int j) {
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(&r);
-        uint32_t x = w[0];
-#pragma unroll
-        for (int i = 1; i < 4; ++i)
-            if (i == j) x = w[i];
-        return __uint_as_float(x);
+        return __uint_as_float(j == 0 ? r.x : j == 1 ? r.y : j == 2 ? r.z : r.w);
     }
     static __device__ __forceinline__ uint4 from_pairs(const uint64_t (&p)[2]) {
         float a, b, c, d;
@@ -159,88 +199,250 @@ struct Vec<float> {
 };
 
 // The aligned 16-byte vectors that cover a row: the row starts `mis` elements into the
-// first one and ends inside the last.
+// first one and ends inside the last.  Vectors b0 .. b1 - 1 lie in it whole.
 template <typename T>
 struct Row {
+    static constexpr int N = Vec<T>::N;
     T *base;  // the first vector (at or before the row's first element)
-    int64_t V, mis, nv;
-    __device__ __forceinline__ Row(T *row, int64_t V_) : V(V_) {
-        mis = static_cast<int64_t>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+    int V, mis, b0, b1;
+    __device__ __forceinline__ Row(T *row, int V_) : V(V_) {
+        mis = static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
         base = row - mis;
-        nv = (mis + V + Vec<T>::N - 1) / Vec<T>::N;
+        b0 = mis ? 1 : 0;
+        b1 = max(static_cast<int>((static_cast<uint32_t>(mis) + static_cast<uint32_t>(V)) / N), b0);
     }
-    __device__ __forceinline__ bool full(int64_t v) const {
-        return v * Vec<T>::N >= mis && (v + 1) * Vec<T>::N <= mis + V;
+    __device__ __forceinline__ const uint4 *vec(int v) const { return reinterpret_cast<const uint4 *>(base) + v; }
+    // A vector that the row shares with its neighbours: thread 0 has the first, thread 1
+    // the last.  False where there is none.
+    __device__ __forceinline__ bool edge(int &v) const {
+        v = threadIdx.x == 0 ? 0 : b1;
+        if (threadIdx.x == 0) return mis != 0;
+        return threadIdx.x == 1 && static_cast<int64_t>(b1) * N < static_cast<int64_t>(mis) + V;
     }
-    // Vector v; elements outside the row read as -inf and are not touched in memory.
-    __device__ __forceinline__ uint4 load(int64_t v) const {
-        uint4 r;
-        if (full(v)) {
-            const T *p = base + v * Vec<T>::N;
-            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                         : "l"(p)
-                         : "memory");
-        } else {
-            r = make_uint4(Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill);
-            for (int j = 0; j < Vec<T>::N; ++j) {
-                const int64_t e = v * Vec<T>::N + j;
-                if (e >= mis && e < mis + V) Vec<T>::set(r, j, Vec<T>::raw(base + e));
-            }
-        }
+    __device__ __forceinline__ bool has(int v, int j) const {
+        const int64_t e = static_cast<int64_t>(v) * N + j;
+        return e >= mis && e < static_cast<int64_t>(mis) + V;
+    }
+    // an edge vector; elements outside the row read as -inf and are not touched in memory
+    __device__ __forceinline__ uint4 load_edge(int v) const {
+        uint4 r = make_uint4(Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill);
+        for (int j = 0; j < N; ++j)
+            if (has(v, j)) Vec<T>::set(r, j, Vec<T>::raw(base + static_cast<int64_t>(v) * N + j));
         return r;
     }
-    __device__ __forceinline__ void store(int64_t v, const uint4 &r) const {
-        if (full(v)) {
-            *reinterpret_cast<uint4 *>(base + v * Vec<T>::N) = r;
-        } else {
-            for (int j = 0; j < Vec<T>::N; ++j) {
-                const int64_t e = v * Vec<T>::N + j;
-                if (e >= mis && e < mis + V) Vec<T>::store(base + e, Vec<T>::value(r, j));
-            }
+    __device__ __forceinline__ void store_edge(int v, const uint4 &r) const {
+        for (int j = 0; j < N; ++j)
+            if (has(v, j)) Vec<T>::store(base + static_cast<int64_t>(v) * N + j, Vec<T>::value(r, j));
+    }
+    // index in the row of element j of vector v
+    __device__ __forceinline__ uint32_t index(int v, int j) const {
+        return static_cast<uint32_t>(v) * N + j - mis;
+    }
+};
+
+__device__ __forceinline__ uint4 load_vec(const uint4 *p) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p)
+                 : "memory");
+    return r;
+}
+
+// Vectors v, v + W, ... as far as they are in the row (their number is returned); the
+// others read as -inf.
+template <int W, int U, typename T>
+__device__ __forceinline__ int load_some(const Row<T> &row, int v, uint4 (&r)[U]) {
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const bool in = v + u * W < row.b1;
+        n += in;
+        r[u] = in ? load_vec(row.vec(v + u * W))
+                  : make_uint4(Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill);
+    }
+    return n;
+}
+
+// Walks the row's whole vectors with W threads, U in flight per thread: f(r, v, n) gets
+// vectors v, v + W, ..., of which the first n are in the row (the others read as -inf).
+// n is U, known to the compiler, in all batches of a warp but the last.
+template <int W, int U, typename T, typename F>
+__device__ __forceinline__ void walk_body(const Row<T> &row, F &&f) {
+    const int tid = threadIdx.x;
+    int v = row.b0 + tid;
+    const int last = row.b1 - 1 - (U - 1) * W - (31 - (tid & 31));
+    for (; v <= last; v += U * W) {
+        uint4 r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) r[u] = load_vec(row.vec(v + u * W));
+        f(r, v, std::integral_constant<int, U>());
+    }
+    if (v - (tid & 31) < row.b1) {
+        uint4 r[U];
+        const int n = load_some<W, U>(row, v, r);
+        f(r, v, n);
+    }
+}
+
+// ------------------------------------------------------------------ the ring
+// A row's whole vectors come to the walking warps through a ring of chunks in shared
+// memory, filled by bulk copies that one thread issues.  The copies run ahead of the
+// walk by the whole ring, into the next row too, so that memory stays busy while the
+// block joins its sums, ranks alternatives or finishes a loss.
+struct RingCtl {
+    uint64_t full[kStages], empty[kStages];
+    int abort_flag;
+};
+
+// Position in the ring; producer and walkers take the same steps.
+struct RingPos {
+    int stage = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++stage == kStages) {
+            stage = 0;
+            phase ^= 1u;
         }
     }
 };
 
+__device__ __forceinline__ void ring_init(RingCtl &ctl) {
+    for (int i = 0; i < kStages; ++i) {
+        mbar_init(&ctl.full[i], 1);
+        mbar_init(&ctl.empty[i], kWarps);
+    }
+    ctl.abort_flag = 0;
+    fence_mbarrier_init();
+}
+
+template <typename T>
+__device__ __forceinline__ int chunks_of(const Row<T> &row) {
+    return (row.b1 - row.b0 + kChunk - 1) / kChunk;
+}
+
+// One thread: the row's chunks, once.  A wait that runs out raises the block's abort
+// flag, after which every wait returns at once: the block runs to its end on what the
+// ring holds, and the device error word tells.
+template <typename T>
+__device__ __forceinline__ void ring_fill(const Row<T> &row, uint4 *ring, RingCtl &ctl, RingPos &pos, int *err) {
+    const int chunks = chunks_of(row);
+    for (int c = 0; c < chunks; ++c, pos.next()) {
+        if (!mbar_wait_bounded(&ctl.empty[pos.stage], pos.phase ^ 1u, &ctl.abort_flag, err, kWaitLimitNs)) return;
+        const int v = row.b0 + c * kChunk;
+        const uint32_t bytes = static_cast<uint32_t>(min(kChunk, row.b1 - v)) * 16u;
+        mbar_arrive_expect_tx(&ctl.full[pos.stage], bytes);
+        asm volatile(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                smem_u32(ring + pos.stage * kChunk)),
+            "l"(row.vec(v)), "r"(bytes), "r"(smem_u32(&ctl.full[pos.stage]))
+            : "memory");
+    }
+}
+
+// After an abort: copies still in flight land before the block exits (a fixed 2 ms; their
+// barriers may not be asked, since the walkers' phases have come apart).
+__device__ __forceinline__ void ring_end(RingCtl &ctl) {
+    if (*static_cast<volatile int *>(&ctl.abort_flag)) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 2000000ull) {
+        }
+    }
+}
+
+// The walkers: f(r, v, n) for each chunk, with vectors v, v + kThreads, ... of which the
+// first n are in the row (the others read as -inf); n is kUnroll, known to the compiler,
+// in whole chunks.
+template <typename T, typename F>
+__device__ __forceinline__ void ring_walk(const Row<T> &row, const uint4 *ring, RingCtl &ctl, RingPos &pos, int *err,
+                                          F &&f) {
+    const int tid = threadIdx.x, chunks = chunks_of(row);
+#pragma unroll 1
+    for (int c = 0; c < chunks; ++c, pos.next()) {
+        (void)mbar_wait_bounded(&ctl.full[pos.stage], pos.phase, &ctl.abort_flag, err, kWaitLimitNs);
+        const uint4 *src = ring + pos.stage * kChunk + tid;
+        const int v = row.b0 + c * kChunk + tid;
+        uint4 r[kUnroll];
+        if (row.b0 + (c + 1) * kChunk <= row.b1) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) r[u] = src[u * kThreads];
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(&ctl.empty[pos.stage]);
+            f(r, v, std::integral_constant<int, kUnroll>());
+        } else {
+            int n = 0;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const bool in = v + u * kThreads < row.b1;
+                n += in;
+                r[u] = in ? src[u * kThreads] : make_uint4(Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill);
+            }
+            __syncwarp();
+            if ((tid & 31) == 0) mbar_arrive(&ctl.empty[pos.stage]);
+            f(r, v, n);
+        }
+    }
+}
+
+// Barriers of the first P threads of the block (the producer warp takes no part).
+template <int P>
+__device__ __forceinline__ void bar() {
+    asm volatile("bar.sync 1, %0;" ::"n"(P) : "memory");
+}
+template <int P>
+__device__ __forceinline__ bool bar_or(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
+        "setp.ne.u32 p, %1, 0;\n"
+        "bar.red.or.pred q, 1, %2, p;\n"
+        "selp.u32 %0, 1, 0, q;\n"
+        "}\n"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(x)), "n"(P)
+        : "memory");
+    return r != 0;
+}
+
 // ------------------------------------------------------------------ running softmax sums
 
-// m is finite from the start (the type's lowest value), so that x - m is -inf, never
-// NaN, for a masked entry.  A NaN or +inf entry makes S NaN and stays.
+// A NaN or +inf entry makes S NaN and stays.
 template <bool ENT>
 struct Sums {
-    float m = -FLT_MAX;
+    float m = kFloor;
+    float mu;  // RN(m c), what y is measured from
     uint64_t S = 0, A = 0;  // two partial sums each
 
+    __device__ __forceinline__ explicit Sums(float c) : mu(kFloor * c) {}
+
     template <typename T, int U>
-    __device__ __forceinline__ void add(const uint4 (&r)[U], float c) {
-        float mx = Vec<T>::max(r[0]);
-#pragma unroll
-        for (int u = 1; u < U; ++u) mx = fmaxf(mx, Vec<T>::max(r[u]));
+    __device__ __forceinline__ float add(const uint4 (&r)[U], float c) {
+        const float mx = Vec<T>::max(r);
         if (mx > m) {
-            const float g = fmaxf((m - mx) * c, -1e4f), f = ex2(g);
+            const float mu_new = mx * c, g = fmaxf(mu - mu_new, -1e4f), f = ex2(g);
             const uint64_t f2 = f2_pack(f, f);
             if (ENT) A = f2_mul(f2_fma(S, f2_pack(g, g), A), f2);
             S = f2_mul(S, f2);
             m = mx;
+            mu = mu_new;
         }
-        const uint64_t nm = f2_pack(-m, -m), c2 = f2_pack(c, c);
+        const uint64_t nmu = f2_pack(-mu, -mu), c2 = f2_pack(c, c);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             uint64_t p[Vec<T>::N / 2];
-            Vec<T>::pairs(r[u], p);
+            Vec<T>::pairs(ENT ? Vec<T>::clamp(r[u]) : r[u], p);  // 0 times -inf would be NaN in A
 #pragma unroll
             for (int i = 0; i < Vec<T>::N / 2; ++i) {
+                const uint64_t y = f2_fma(p[i], c2, nmu);
                 float a, b;
-                f2_unpack(f2_mul(f2_add(p[i], nm), c2), a, b);
-                if (ENT) {  // 2^-200 is 0 in fp32, and 0 times -200 is 0
-                    a = max_nan(a, -200.0f);
-                    b = max_nan(b, -200.0f);
-                }
+                f2_unpack(y, a, b);
                 const uint64_t e = f2_pack(ex2(a), ex2(b));
                 S = f2_add(S, e);
-                if (ENT) A = f2_fma(e, f2_pack(a, b), A);
+                if (ENT) A = f2_fma(e, y, A);
             }
         }
+        return mx;
     }
 };
 
@@ -258,48 +460,105 @@ __device__ __forceinline__ RowSums join(const RowSums &a, const RowSums &b, floa
     return r;
 }
 
-// The block's sums, in every thread; `buf` holds kWarps entries.  The join over lanes
-// is a butterfly (the two sides of a pair differ in operand order only, and join is
-// symmetric up to the order of one addition), the join over warps runs in order.
-template <bool ENT>
-__device__ __forceinline__ RowSums block_join(const Sums<ENT> &s, float c, RowSums *buf) {
-    RowSums r;
-    float lo, hi;
-    r.m = s.m;
-    f2_unpack(s.S, lo, hi);
-    r.S = lo + hi;
-    f2_unpack(s.A, lo, hi);
-    r.A = lo + hi;
+// Sums of 2 * HALF lanes, in each of them: the maximum first, then one factor per lane,
+// then a butterfly of additions (whose order is the same in every lane of a group).
+template <int HALF, bool ENT>
+__device__ __forceinline__ RowSums lanes_join(RowSums r, float c) {
+    float m = r.m;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        RowSums o;
-        o.m = __shfl_xor_sync(0xffffffffu, r.m, off);
-        o.S = __shfl_xor_sync(0xffffffffu, r.S, off);
-        o.A = __shfl_xor_sync(0xffffffffu, r.A, off);
-        r = join(r, o, c);
+    for (int off = HALF; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float g = fmaxf((r.m - m) * c, -1e4f), f = ex2(g);
+    r.m = m;
+    if (ENT) r.A = f * fmaf(r.S, g, r.A);
+    r.S *= f;
+#pragma unroll
+    for (int off = HALF; off > 0; off >>= 1) {
+        r.S += __shfl_xor_sync(0xffffffffu, r.S, off);
+        if (ENT) r.A += __shfl_xor_sync(0xffffffffu, r.A, off);
     }
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = r;
-    __syncthreads();
-    r = buf[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) r = join(r, buf[w], c);
     return r;
 }
 
-template <bool ENT, typename T>
-__device__ __forceinline__ Sums<ENT> walk_sums(const Row<T> &row, float c) {
-    Sums<ENT> s;
-    for (int64_t v = threadIdx.x; v < row.nv; v += kThreads * kUnroll) {
-        uint4 r[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-            r[u] = v + u * kThreads < row.nv
-                       ? row.load(v + u * kThreads)
-                       : make_uint4(Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill);
-        s.template add<T, kUnroll>(r, c);
-    }
-    return s;
+// A warp's sums, in all its lanes.
+template <bool ENT>
+__device__ __forceinline__ RowSums warp_join(const Sums<ENT> &s, float c) {
+    RowSums r;
+    float lo, hi;
+    r.m = s.m;
+    const float off_mu = fmaf(s.m, c, -s.mu);  // y is too large by this
+    const float f = ex2(-off_mu);
+    f2_unpack(s.S, lo, hi);
+    const float S = lo + hi;
+    f2_unpack(s.A, lo, hi);
+    r.S = S == 0.0f ? 0.0f : S * f;  // without an entry, kFloor c is rounded by more than ex2 can say
+    r.A = S == 0.0f ? 0.0f : (lo + hi - off_mu * S) * f;
+    return lanes_join<16, ENT>(r, c);
 }
+
+// The sums of W warps (a power of two of entries, of which the first W count), in every thread.
+template <int W, bool ENT>
+__device__ __forceinline__ RowSums warps_join(const RowSums *buf, float c) {
+    constexpr int P = W <= 8 ? 8 : 16;
+    static_assert(W <= 16, "at most sixteen warps");
+    const int i = threadIdx.x & (P - 1);
+    RowSums r{kFloor, 0.0f, 0.0f};
+    if (i < W) r = buf[i];
+    return lanes_join<P / 2, ENT>(r, c);
+}
+
+// The sums of a row whose fast walk gave 0 or no finite sum, with the row's own maximum
+// taken off first.  `keep(index)` leaves entries out.  The block's first THREADS threads
+// call it; the maximum is that of all of them, so that the
+// parts are added without another factor.
+template <int THREADS, typename T, typename Keep>
+__device__ __noinline__ RowSums far_sums(const Row<T> row, float c, RowSums *buf, Keep keep) {
+    constexpr int WARPS = THREADS / 32;
+    float m = -INFINITY;
+    bool nan = false;
+    for (int e = threadIdx.x; e < row.V; e += THREADS)
+        if (keep(e)) {
+            const float x = Vec<T>::load(row.base + row.mis + e);
+            nan = nan || isnan(x);
+            m = fmaxf(m, x);
+        }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    nan = bar_or<THREADS>(nan);
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5].m = m;
+    bar<THREADS>();
+    for (int w = 0; w < WARPS; ++w) m = fmaxf(m, buf[w].m);
+    bar<THREADS>();
+    RowSums r{fmaxf(m, -FLT_MAX), 0.0f, 0.0f};
+    if (nan || m == INFINITY) {
+        r.S = NAN;
+        return r;
+    }
+    for (int e = threadIdx.x; e < row.V; e += THREADS)
+        if (keep(e)) {
+            const float x = Vec<T>::load(row.base + row.mis + e);
+            if (x > -INFINITY) {
+                const float y = fmaxf((x - r.m) * c, -1e4f), t = ex2(y);
+                r.S += t;
+                r.A = fmaf(t, y, r.A);
+            }
+        }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        r.S += __shfl_xor_sync(0xffffffffu, r.S, off);
+        r.A += __shfl_xor_sync(0xffffffffu, r.A, off);
+    }
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = r;
+    bar<THREADS>();
+    r.S = r.A = 0.0f;
+    for (int w = 0; w < WARPS; ++w) {
+        r.S += buf[w].S;
+        r.A += buf[w].A;
+    }
+    bar<THREADS>();
+    return r;
+}
+
+__device__ __forceinline__ bool is_far(const RowSums &s) { return s.S == 0.0f || !(s.S < INFINITY); }
 
 // ------------------------------------------------------------------ log probabilities
 
@@ -313,6 +572,7 @@ struct LogprobArgs {
     float *logprob, *entropy;
     int64_t *top_ids;
     float *top_logprobs;
+    int *err;
 };
 
 // An order-keeping key of a logit (never NaN here): larger value, larger key; -0 is 0.
@@ -325,167 +585,274 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 struct TopShared {
-    uint64_t cand[kCandidates];  // key << 32 | ~index: unique, larger = earlier
-    float gmax[kThreads];
-    float threshold;
-    int count;
+    int vecs[kCandidates];   // vectors with an entry that reached the walk's bound
+    alignas(16) uint64_t kept[kKept];  // entries that reach the row's last bound: key << 32 | ~index
+    uint32_t max_key[kThreads];
+    double logS;
+    float bound;
+    int count, kept_count;
     int warp_count[kWarps];
 };
 
 // Elements of the row for which pred(key, index) holds, counted over the block.
 template <typename T, typename Pred>
-__device__ int64_t block_count(const Row<T> &row, TopShared &sh, Pred pred) {
+__device__ __forceinline__ int64_t block_count(const Row<T> &row, TopShared &sh, Pred pred) {
     int n = 0;
-    for (int64_t v = threadIdx.x; v < row.nv; v += kThreads) {
-        const uint4 r = row.load(v);
-#pragma unroll
-        for (int j = 0; j < Vec<T>::N; ++j) {
-            const float x = Vec<T>::value(r, j);
-            n += x > -INFINITY && pred(order_key(x), static_cast<uint32_t>(v * Vec<T>::N + j - row.mis));
-        }
+    for (int i = threadIdx.x; i < row.V; i += kThreads) {
+        const float x = Vec<T>::load(row.base + row.mis + i);
+        n += x > -INFINITY && pred(order_key(x), static_cast<uint32_t>(i));
     }
     n = __reduce_add_sync(0xffffffffu, n);
-    __syncthreads();
+    bar<kThreads>();
     if ((threadIdx.x & 31) == 0) sh.warp_count[threadIdx.x >> 5] = n;
-    __syncthreads();
+    bar<kThreads>();
     int64_t total = 0;
     for (int w = 0; w < kWarps; ++w) total += sh.warp_count[w];
     return total;
 }
 
-// The k largest (value, lowest index first) of a row without NaN or +inf.  The k-th
-// largest of at least k thread (or thread-group) maxima is a bound that at least k
-// elements reach; what reaches it, usually about 1.4 k elements, is collected in
-// shared memory and ranked by counting.  Where ties or an uneven row make that more
-// than the buffer, the k-th key and then the last index of its ties are found bit by
-// bit with one walk each.
+// The k first entries of a row with too many that reach any simple bound (ties): the
+// k-th key, then the last index of its ties, are found bit by bit with one walk each,
+// and exactly k entries collected.
 template <typename T>
-__device__ void top_k(const Row<T> &row, const LogprobArgs &a, int64_t t, float thread_max, float m, double logS,
-                      TopShared &sh) {
+__device__ __noinline__ void top_k_by_bits(const Row<T> row, int k, TopShared &sh) {
+    uint32_t key = 0;
+    for (int b = 31; b >= 0; --b) {
+        const uint32_t cand = key | (1u << b);
+        if (block_count(row, sh, [=](uint32_t q, uint32_t) { return q >= cand; }) >= k) key = cand;
+    }
+    const int64_t need = k - block_count(row, sh, [=](uint32_t q, uint32_t) { return q > key; });
+    // the largest index bound that still leaves fewer than the needed ties before it
+    uint32_t last = 0;
+    for (int b = 31; b >= 0; --b) {
+        const uint32_t cand = last | (1u << b);
+        if (cand <= static_cast<uint32_t>(row.V - 1) &&
+            block_count(row, sh, [=](uint32_t q, uint32_t i) { return q == key && i < cand; }) < need)
+            last = cand;
+    }
+    bar<kThreads>();
+    if (threadIdx.x == 0) sh.kept_count = 0;
+    bar<kThreads>();
+    for (int i = threadIdx.x; i < row.V; i += kThreads) {
+        const float x = Vec<T>::load(row.base + row.mis + i);
+        const uint32_t q = order_key(x), idx = static_cast<uint32_t>(i);
+        if (x > -INFINITY && (q > key || (q == key && idx <= last)))
+            sh.kept[atomicAdd(&sh.kept_count, 1)] = (static_cast<uint64_t>(q) << 32) | ~idx;
+    }
+    bar<kThreads>();
+}
+
+// A value that at least k entries walked so far reach (-FLT_MAX while there are fewer):
+// the k-th largest of the threads' maxima, to its upper 16 bits, found by one warp with a
+// bisection on the counts, over the bits in which the maxima differ.
+__device__ __forceinline__ float refresh_bound(float thread_max, int k, TopShared &sh) {
+    sh.max_key[threadIdx.x] = order_key(thread_max);
+    bar<kThreads>();
+    if (threadIdx.x < 32) {
+        uint32_t q[kThreads / 32], lo = 0xFFFFFFFFu, hi = 0;
+#pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {
+            q[i] = sh.max_key[threadIdx.x + 32 * i];
+            lo = min(lo, q[i]);
+            hi = max(hi, q[i]);
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        const int top = 31 - __clz(static_cast<int>(lo ^ hi));  // the highest bit that differs; -1: none
+        uint32_t t = top < 31 ? hi & ~((2u << top) - 1u) : 0u;
+        if (top < 0) t = hi;
+#pragma unroll 1
+        for (int b = top; b >= 16; --b) {
+            const uint32_t cand = t | (1u << b);
+            uint32_t n = 0;
+#pragma unroll
+            for (int i = 0; i < kThreads / 32; ++i) n += q[i] >= cand;
+            if (__reduce_add_sync(0xffffffffu, n) >= static_cast<uint32_t>(k)) t = cand;
+        }
+        // a thread without an entry above kFloor says about kFloor: no bound then
+        const float v = key_value(t);
+        if (threadIdx.x == 0) sh.bound = v > 0.5f * kFloor ? v : -FLT_MAX;
+    }
+    bar<kThreads>();
+    return sh.bound;
+}
+
+// Notes vector v if one of its entries reaches the bound.
+template <typename T>
+__device__ __forceinline__ void note(const uint4 &r, int v, float bound, TopShared &sh) {
+    if (Vec<T>::max(r) >= bound) {  // NaN and -inf never do
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < kCandidates) sh.vecs[at] = v;
+    }
+}
+
+// The walk for the sums, which also notes the vectors that may hold alternatives: those
+// with an entry that reaches a bound, refreshed each time the part walked has doubled.
+// For a row in random order these are about k log2(batches) vectors.
+template <typename T>
+__device__ __forceinline__ Sums<true> walk_candidates(const Row<T> &row, const LogprobArgs &a, const uint4 *ring,
+                                                      RingCtl &ctl, RingPos &pos, TopShared &sh) {
+    Sums<true> s(a.c);
+    if (threadIdx.x == 0) sh.count = sh.kept_count = 0;
+    float bound = -FLT_MAX;
+    int ve, done = 0;
+    const bool edge = row.edge(ve);
+    if (edge) {
+        uint4 r[1] = {row.load_edge(ve)};
+        s.template add<T, 1>(r, a.c);
+    }
+    ring_walk(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int) {
+        const float mx = s.template add<T, kUnroll>(r, a.c);
+        if ((done & (done + 1)) == 0) bound = refresh_bound(s.m, a.k, sh);  // 1, 2, 4, ... chunks walked
+        ++done;
+        if (mx >= bound) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) note<T>(r[u], v + u * kThreads, bound, sh);
+        }
+    });
+    if (done == 0) bound = refresh_bound(s.m, a.k, sh);  // a row within two vectors
+    if (edge) note<T>(row.load_edge(ve), ve, bound, sh);
+    return s;
+}
+
+// The k largest (value, lowest index first) of a row without NaN or +inf, from the
+// vectors noted in its walk: their entries that reach the row's last bound are ranked by
+// counting.
+template <typename T>
+__device__ __forceinline__ void top_k(const Row<T> &row, const LogprobArgs &a, int64_t t, float thread_max, float m,
+                                      TopShared &sh) {
     const int tid = threadIdx.x, k = a.k;
-    // groups of threads, a power of two at least twice k
-    int group = 1;
-    while (kThreads / (2 * group) >= 2 * k && group < 32) group *= 2;
-    float g = thread_max;
-    for (int off = 1; off < group; off *= 2) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, off));
-    const int ng = kThreads / group;
-    if ((tid & (group - 1)) == 0) sh.gmax[tid / group] = g;
-    if (tid == 0) sh.count = 0;
-    __syncthreads();
-    if (tid < ng) {
-        const float mine = sh.gmax[tid];
-        int rank = 0;
-        for (int j = 0; j < ng; ++j) {
-            const float o = sh.gmax[j];
-            rank += o > mine || (o == mine && j < tid);
-        }
-        if (rank == k - 1) sh.threshold = mine;
-    }
-    __syncthreads();
-    const float thr = sh.threshold;
-    for (int64_t v = tid; v < row.nv; v += kThreads) {
-        const uint4 r = row.load(v);
-        if (Vec<T>::max(r) >= thr) {
-#pragma unroll
-            for (int j = 0; j < Vec<T>::N; ++j) {
-                const float x = Vec<T>::value(r, j);
-                if (x >= thr && x > -INFINITY) {
-                    const int at = atomicAdd(&sh.count, 1);
-                    const uint32_t idx = static_cast<uint32_t>(v * Vec<T>::N + j - row.mis);
-                    if (at < kCandidates) sh.cand[at] = (static_cast<uint64_t>(order_key(x)) << 32) | ~idx;
-                }
-            }
-        }
-    }
-    __syncthreads();
-    int n = sh.count;
-    if (n > kCandidates) {
-        uint32_t key = 0;
-        for (int b = 31; b >= 0; --b) {
-            const uint32_t cand = key | (1u << b);
-            if (block_count(row, sh, [=](uint32_t q, uint32_t) { return q >= cand; }) >= k) key = cand;
-        }
-        const int64_t above = block_count(row, sh, [=](uint32_t q, uint32_t) { return q > key; });
-        // the largest index bound that still leaves fewer than the needed ties before it
-        const int64_t need = k - above;
-        uint32_t last = 0;
-        for (int b = 31; b >= 0; --b) {
-            const uint32_t cand = last | (1u << b);
-            if (cand <= static_cast<uint32_t>(a.V - 1) &&
-                block_count(row, sh, [=](uint32_t q, uint32_t i) { return q == key && i < cand; }) < need)
-                last = cand;
-        }
-        __syncthreads();
+    const float bound = refresh_bound(thread_max, k, sh);  // its barriers also end the walk's notes
+    if (sh.count > kCandidates) {  // a row that rises along the walk: note again, by the last bound
+        bar<kThreads>();
         if (tid == 0) sh.count = 0;
-        __syncthreads();
-        for (int64_t v = tid; v < row.nv; v += kThreads) {
-            const uint4 r = row.load(v);
+        bar<kThreads>();
+        walk_body<kThreads, kUnroll>(row, [&](uint4(&r)[kUnroll], int v, int) {
 #pragma unroll
-            for (int j = 0; j < Vec<T>::N; ++j) {
-                const float x = Vec<T>::value(r, j);
-                const uint32_t q = order_key(x), idx = static_cast<uint32_t>(v * Vec<T>::N + j - row.mis);
-                if (x > -INFINITY && (q > key || (q == key && idx <= last)))
-                    sh.cand[atomicAdd(&sh.count, 1)] = (static_cast<uint64_t>(q) << 32) | ~idx;
+            for (int u = 0; u < kUnroll; ++u) note<T>(r[u], v + u * kThreads, bound, sh);
+        });
+        int ve;
+        if (row.edge(ve)) note<T>(row.load_edge(ve), ve, bound, sh);
+        bar<kThreads>();
+    }
+    for (int i = tid; i < min(sh.count, kCandidates); i += kThreads) {
+        const int v = sh.vecs[i];
+        const uint4 r = v >= row.b0 && v < row.b1 ? load_vec(row.vec(v)) : row.load_edge(v);
+#pragma unroll
+        for (int j = 0; j < Vec<T>::N; ++j) {
+            const float x = Vec<T>::value(r, j);
+            if (x >= bound) {
+                const int at = atomicAdd(&sh.kept_count, 1);
+                if (at < kKept) sh.kept[at] = (static_cast<uint64_t>(order_key(x)) << 32) | ~row.index(v, j);
             }
         }
-        __syncthreads();
-        n = sh.count;  // exactly k
     }
+    bar<kThreads>();
+    if (sh.count > kCandidates || sh.kept_count > kKept) top_k_by_bits(row, k, sh);
+    const int n = sh.kept_count;
     for (int i = tid; i < n; i += kThreads) {
-        const uint64_t mine = sh.cand[i];
+        const uint64_t mine = sh.kept[i];
         int rank = 0;
-        for (int j = 0; j < n; ++j) rank += sh.cand[j] > mine;
+        int j = 0;
+#pragma unroll 4
+        for (; j + 2 <= n; j += 2) {
+            const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(&sh.kept[j]);
+            rank += (o.x > mine) + (o.y > mine);
+        }
+        if (j < n) rank += sh.kept[j] > mine;
         if (rank < k) {
             a.top_ids[t * k + rank] = static_cast<int64_t>(~static_cast<uint32_t>(mine));
             const float x = key_value(static_cast<uint32_t>(mine >> 32));
-            a.top_logprobs[t * k + rank] = static_cast<float>((static_cast<double>(x) - m) * a.inv_tau - logS);
+            a.top_logprobs[t * k + rank] = static_cast<float>((static_cast<double>(x) - m) * a.inv_tau - sh.logS);
         }
     }
     for (int i = n + tid; i < k; i += kThreads) {
         a.top_ids[t * k + i] = -1;
         a.top_logprobs[t * k + i] = -INFINITY;
     }
-    __syncthreads();
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) k_token_logprobs(const LogprobArgs a) {
-    __shared__ RowSums buf[kWarps];
-    __shared__ TopShared sh;
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) k_token_logprobs(const LogprobArgs a) {
+    extern __shared__ __align__(128) uint4 ring[];
+    __shared__ RowSums buf[2][kWarps];  // in turn, so that a row's readers need no barrier before the next row
+    __shared__ RingCtl ctl;
+    __shared__ typename std::conditional<TOP, TopShared, int>::type sh;
+    if (threadIdx.x == 0) ring_init(ctl);
+    __syncthreads();
     pdl_wait();
     pdl_allow_dependents();
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        T *p = const_cast<T *>(static_cast<const T *>(a.x)) + t * a.ld;
-        const Row<T> row(p, a.V);
-        const Sums<true> mine = walk_sums<true>(row, a.c);
-        const RowSums s = block_join(mine, a.c, buf);
-        const bool none = s.S == 0.0f, bad = !(s.S >= 0.0f) || s.S == INFINITY;
-        const double logS = log(static_cast<double>(s.S));
-        if (threadIdx.x == 0) {
-            const int64_t id = a.targets[t];
-            float lp = 0.0f;
-            if (id >= a.V)
-                lp = NAN;
-            else if (id >= 0)
-                lp = none ? -INFINITY
-                          : static_cast<float>((static_cast<double>(Vec<T>::load(p + id)) - s.m) * a.inv_tau - logS);
-            if (bad && id >= 0) lp = NAN;
-            a.logprob[t] = lp;
-            // H = -sum p ln p = ln S - ln 2 (A / S)
-            a.entropy[t] = none ? 0.0f
-                                : static_cast<float>(logS - 0.69314718055994530942 * (static_cast<double>(s.A) / s.S));
+    RingPos pos;
+    auto row_of = [&](int64_t t) {
+        return Row<T>(const_cast<T *>(static_cast<const T *>(a.x)) + t * a.ld, static_cast<int>(a.V));
+    };
+    if (threadIdx.x >= kThreads) {
+        if (threadIdx.x == kThreads) {
+            for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) ring_fill(row_of(t), ring, ctl, pos, a.err);
+            ring_end(ctl);
         }
-        if (a.k > 0) {
+        return;
+    }
+    int turn = 0;
+    // the target comes a row ahead, and its logit while the row is walked
+    int64_t id = threadIdx.x == 0 ? a.targets[blockIdx.x] : -1, next_id = -1;
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1, id = next_id) {
+        const Row<T> row = row_of(t);
+        float xt = 0.0f;
+        if (id >= 0 && id < a.V) xt = Vec<T>::load(row.base + row.mis + id);
+        if (threadIdx.x == 0 && t + gridDim.x < a.T) next_id = a.targets[t + gridDim.x];
+        const Sums<true> mine = [&] {
+            if constexpr (TOP) {
+                return walk_candidates(row, a, ring, ctl, pos, sh);
+            } else {
+                Sums<true> s(a.c);
+                ring_walk(row, ring, ctl, pos, a.err,
+                          [&](uint4(&r)[kUnroll], int, int) { s.template add<T, kUnroll>(r, a.c); });
+                int v;
+                if (row.edge(v)) {
+                    uint4 r[1] = {row.load_edge(v)};
+                    s.template add<T, 1>(r, a.c);
+                }
+                return s;
+            }
+        }();
+        const RowSums w = warp_join(mine, a.c);
+        if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = w;
+        bar<kThreads>();
+        RowSums s = warps_join<kWarps, true>(buf[turn], a.c);
+        if (is_far(s)) {
+            bar<kThreads>();
+            s = far_sums<kThreads>(row, a.c, buf[turn], [](int) { return true; });
+        }
+        const bool none = s.S == 0.0f, bad = !(s.S < INFINITY);
+        if (threadIdx.x < 32) {
+            const double logS = log(static_cast<double>(s.S));
+            if (threadIdx.x == 0) {
+                float lp = 0.0f;
+                if (id >= 0) {
+                    if (bad || id >= a.V)
+                        lp = NAN;
+                    else
+                        lp = none ? -INFINITY : static_cast<float>((static_cast<double>(xt) - s.m) * a.inv_tau - logS);
+                }
+                a.logprob[t] = lp;
+                // H = -sum p ln p = ln S - ln 2 (A / S)
+                a.entropy[t] =
+                    none ? 0.0f : static_cast<float>(logS - 0.69314718055994530942 * (static_cast<double>(s.A) / s.S));
+                if constexpr (TOP) sh.logS = logS;  // before the barriers of top_k
+            }
+        }
+        if constexpr (TOP) {
             if (bad || none) {
                 for (int i = threadIdx.x; i < a.k; i += kThreads) {
                     a.top_ids[t * a.k + i] = -1;
                     a.top_logprobs[t * a.k + i] = bad ? NAN : -INFINITY;
                 }
             } else {
-                top_k(row, a, t, mine.m, s.m, logS, sh);
+                top_k(row, a, t, mine.m, s.m, sh);
             }
+            bar<kThreads>();  // the next row's walk clears the counts
         }
-        __syncthreads();  // buf is written again by the next row
     }
 }
 
@@ -502,14 +869,21 @@ struct DistillArgs {
     const float *weight;  // nullable: 1
     float *loss;          // nullable
     void *dx;             // nullable; may be x
+    int *err;
 };
 
+// A row's slots, and what its teacher and its slots alone say.
 struct Slots {
     int id[kTopMax];  // -1: empty
-    float x[kTopMax], tl[kTopMax], q[kTopMax], grad[kTopMax];
+    float x[kTopMax], tl[kTopMax], q[kTopMax];
     bool first[kTopMax];  // the slot that stands for its id where an id is given twice
-    float coef;
-    int zero;
+    float w;              // the row's weight
+    RowSums own;          // sums over the slots (each id once)
+    double logq0;         // ln q_i = tl_i - logq0
+    double qr;            // the teacher's mass outside the slots (TAIL)
+    bool dup;             // an id is given twice
+    bool bad;             // the row's loss and gradient are NaN, by its teacher
+    bool empty;           // no teacher: no loss
 };
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -518,221 +892,366 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-// One warp: the teacher's masses, the loss and the gradient's constants of a row.
-// With z = x / temperature, p = softmax(z), q the teacher's masses on the slots:
-//   L = sum_i q_i (ln q_i - ln p_i)  [+ q_r (ln q_r - ln p_r)]
-//   dL/dz_j = p_j - q_j on a slot, p_j [(1 - q_r / p_r)] elsewhere.
-// `s` are the sums over the row (renormalised teacher) or over the entries outside the
-// slots (TAIL): p_r is then a sum of its own and not 1 minus the slots' masses, which
-// would cancel when nearly all mass is on the slots.
-template <bool TAIL>
-__device__ void finish_slots(const DistillArgs &a, Slots &sl, const RowSums &s, bool bad_id, bool dup, float w,
-                             float *loss) {
-    const int lane = threadIdx.x & 31, k = a.k;
-    // teacher
-    float tm = -INFINITY;
-    bool any = false, tnan = false;
-    for (int i = lane; i < k; i += 32)
-        if (sl.id[i] >= 0) {
-            tm = fmaxf(tm, sl.tl[i]);
-            any = any || sl.tl[i] > -INFINITY;
-            tnan = tnan || isnan(sl.tl[i]);
-        }
+// A lane's slots of a row as they come from memory, asked for a row before they are used.
+struct RawSlots {
+    static constexpr int PER = kTopMax / 32;
+    int64_t id[PER];
+    float tl[PER], w;
+    __device__ __forceinline__ void fetch(const DistillArgs &a, int64_t t) {
+        const int lane = threadIdx.x & 31;
+        w = 0.0f;
+        if (t >= a.T) return;
+        w = a.weight ? a.weight[t] : 1.0f;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, off));
-    any = __any_sync(0xffffffffu, any);
-    tnan = __any_sync(0xffffffffu, tnan);
-    const double shift = TAIL || !any ? 0.0 : static_cast<double>(tm);
-    double qsum = 0.0;
-    for (int i = lane; i < k; i += 32)
-        if (sl.id[i] >= 0) qsum += exp(static_cast<double>(sl.tl[i]) - shift);
-    qsum = warp_sum(qsum);
-    tnan = tnan || !(qsum < INFINITY);
-    const double logq0 = TAIL ? 0.0 : shift + log(qsum);  // ln q_i = tl_i - logq0
-    // student: the sums over all entries
-    RowSums all = s;
-    if (TAIL) {
-        RowSums mine{-FLT_MAX, 0.0f, 0.0f};
-        for (int i = lane; i < k; i += 32)
-            if (sl.id[i] >= 0 && sl.first[i]) mine.m = fmaxf(mine.m, sl.x[i]);
-        for (int i = lane; i < k; i += 32)
-            if (sl.id[i] >= 0 && sl.first[i]) mine.S += ex2((sl.x[i] - mine.m) * a.c);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) {
-            RowSums o{__shfl_xor_sync(0xffffffffu, mine.m, off), __shfl_xor_sync(0xffffffffu, mine.S, off), 0.0f};
-            mine = join(mine, o, a.c);
+        for (int i = 0; i < PER; ++i) {
+            const int j = lane + 32 * i;
+            id[i] = j < a.k ? a.ids[t * a.k + j] : -1;
+            tl[i] = j < a.k ? a.tlp[t * a.k + j] : -INFINITY;
         }
-        all = join(s, mine, a.c);
     }
-    const double lnS = log(static_cast<double>(all.S));
-    const double qr = TAIL ? fmax(1.0 - qsum, 0.0) : 0.0;
-    const bool live = TAIL && qr > 0.0 && s.S > 0.0f;
+};
+
+// One warp: a row's slots, marked in the bitmap, and the teacher's side of the loss.
+template <typename T, bool TAIL>
+__device__ void prepare_slots(const DistillArgs &a, int64_t t, const RawSlots &raw, Slots &sl, uint32_t *bitmap) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) sl.w = raw.w;
+    if (raw.w == 0.0f) return;  // nothing of the row is read
+    const T *p = static_cast<const T *>(a.x) + t * a.ld;
+    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+    constexpr int PER = RawSlots::PER;
+    int id[PER];
+    float x[PER], tl[PER];
+    bool first[PER], bad = false, twice = false, any = false;
+    float tm = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        tl[i] = raw.tl[i];
+        bad = bad || raw.id[i] >= a.V;
+        id[i] = raw.id[i] < 0 || raw.id[i] >= a.V ? -1 : static_cast<int>(raw.id[i]);
+        x[i] = id[i] >= 0 ? Vec<T>::load(p + id[i]) : -INFINITY;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        first[i] = false;
+        if (id[i] >= 0) {
+            const uint32_t bit = 1u << ((id[i] + mis) & 31);
+            first[i] = !(atomicOr(&bitmap[(id[i] + mis) >> 5], bit) & bit);
+            twice = twice || !first[i];
+            tm = fmaxf(tm, tl[i]);
+            any = any || tl[i] > -INFINITY;
+            bad = bad || isnan(tl[i]);
+        }
+    }
+    RowSums own{-FLT_MAX, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+        if (first[i]) own.m = fmaxf(own.m, x[i]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, off));
+        own.m = fmaxf(own.m, __shfl_xor_sync(0xffffffffu, own.m, off));
+    }
+    any = __any_sync(0xffffffffu, any);
+    const double shift = TAIL || !any ? 0.0 : static_cast<double>(tm);
+    double e[PER], qsum = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        e[i] = 0.0;
+        if (id[i] >= 0) {
+            e[i] = exp(static_cast<double>(tl[i]) - shift);
+            qsum += e[i];
+        }
+        if (first[i]) own.S += ex2((x[i] - own.m) * a.c);
+    }
+    qsum = warp_sum(qsum);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) own.S += __shfl_xor_sync(0xffffffffu, own.S, off);
+    bad = bad || !(qsum < INFINITY);
+    bad = __any_sync(0xffffffffu, bad);
+    twice = __any_sync(0xffffffffu, twice);
+    const double inv = TAIL ? 1.0 : 1.0 / qsum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int j = lane + 32 * i;
+        sl.id[j] = id[i];
+        sl.x[j] = x[i];
+        sl.tl[j] = tl[i];
+        sl.first[j] = first[i];
+        sl.q[j] = static_cast<float>(e[i] * inv);
+    }
+    if (lane == 0) {
+        sl.own = own;
+        sl.logq0 = TAIL ? 0.0 : shift + log(qsum);
+        sl.qr = TAIL ? fmax(1.0 - qsum, 0.0) : 0.0;
+        sl.dup = twice;
+        sl.bad = bad;
+        sl.empty = !TAIL && !any;
+    }
+    __syncwarp();
+}
+
+// What the walked sums `s` (over the row, or with TAIL over the entries outside the
+// slots) make of a row: all its sums, whether it has a loss, and the gradient's factor.
+//   L = sum_i q_i (ln q_i - ln p_i)  [+ q_r (ln q_r - ln p_r)],  p = softmax(x / temperature)
+//   dL/dz_j = p_j - q_j on a slot, p_j [(1 - q_r / p_r)] elsewhere.
+// p_r comes from a sum of its own and not from 1 minus the slots' masses, which would
+// cancel when nearly all mass is on the slots.
+struct RowState {
+    RowSums all;
+    bool zero, nan, live;
+    float coef;  // dx = coef 2^((x - s.m) c) outside the slots
+};
+
+template <bool TAIL>
+__device__ __forceinline__ RowState row_state(const DistillArgs &a, const Slots &sl, const RowSums &s) {
+    RowState r;
+    r.all = TAIL ? join(s, sl.own, a.c) : s;
+    r.nan = sl.bad || !(r.all.S >= 0.0f);
+    r.zero = !r.nan && (sl.empty || r.all.S == 0.0f);
+    r.live = TAIL && sl.qr > 0.0 && s.S > 0.0f;
+    const float F = ex2(fmaxf((s.m - r.all.m) * a.c, -1e4f));
+    float coef = F / r.all.S;
+    if (r.live) coef -= static_cast<float>(sl.qr) / s.S;
+    r.coef = r.nan ? NAN : sl.w * static_cast<float>(a.inv_tau) * coef;
+    return r;
+}
+
+// One warp: the loss of a row, and the gradient at its slots (in sl.x).
+template <bool TAIL>
+__device__ void finish_slots(const DistillArgs &a, Slots &sl, const RowSums &s, const RowState &r, int64_t t) {
+    const int lane = threadIdx.x & 31, k = a.k;
+    const double lnS = log(static_cast<double>(r.all.S));
+    const double up = static_cast<double>(sl.w) * a.inv_tau, inv_S = 1.0 / static_cast<double>(r.all.S);
     double L = 0.0;
     for (int i = lane; i < k; i += 32) {
         if (sl.id[i] < 0) continue;
-        const double lq = static_cast<double>(sl.tl[i]) - logq0;
-        const double q = exp(lq);
-        sl.q[i] = static_cast<float>(q);
-        if (q > 0.0) L += q * (lq - ((static_cast<double>(sl.x[i]) - all.m) * a.inv_tau - lnS));
+        double q = sl.q[i];
+        const double d = static_cast<double>(sl.x[i]) - r.all.m;
+        if (q > 0.0) L += q * (static_cast<double>(sl.tl[i]) - sl.logq0 - (d * a.inv_tau - lnS));
+        if (sl.first[i]) {
+            if (sl.dup) {  // an id given more than once carries its slots' masses together
+                q = 0.0;
+                for (int j = 0; j < k; ++j)
+                    if (sl.id[j] == sl.id[i]) q += sl.q[j];
+            }
+            sl.x[i] = r.nan ? NAN : static_cast<float>(up * (ex2(static_cast<float>(d) * a.c) * inv_S - q));
+        }
     }
     L = warp_sum(L);
-    if (live)
-        L += qr * (log(qr) - (log(static_cast<double>(s.S)) + (static_cast<double>(s.m) - all.m) * a.inv_tau - lnS));
+    if (r.live)
+        L += sl.qr * (log(sl.qr) - (log(static_cast<double>(s.S)) + (static_cast<double>(s.m) - r.all.m) * a.inv_tau - lnS));
+    if (lane == 0 && a.loss) a.loss[t] = r.zero ? 0.0f : r.nan ? NAN : static_cast<float>(sl.w * L);
     __syncwarp();
-    const double up = static_cast<double>(w) * a.inv_tau;
-    for (int i = lane; i < k; i += 32) {
-        if (sl.id[i] < 0 || !sl.first[i]) continue;
-        double q = sl.q[i];
-        if (dup) {  // an id given more than once carries its slots' masses together
-            q = 0.0;
-            for (int j = 0; j < k; ++j)
-                if (sl.id[j] == sl.id[i]) q += sl.q[j];
+}
+
+template <typename T>
+__device__ __forceinline__ void zero_row(const Row<T> &out) {
+    for (int v = out.b0 + threadIdx.x; v < out.b1; v += kThreads)
+        *const_cast<uint4 *>(out.vec(v)) = make_uint4(0, 0, 0, 0);
+    int v;
+    if (out.edge(v)) out.store_edge(v, make_uint4(0, 0, 0, 0));
+}
+
+// Warps 0..7 walk; warp 8 looks after the slots: while the others walk a row for its
+// sums it prepares the next row's, and while they walk it again for the gradient it works
+// out the loss and the gradient at the slots, which it writes when they have passed.
+// Warp 9 fills the ring.
+template <typename T, bool TAIL>
+__global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const DistillArgs a) {
+    extern __shared__ __align__(128) uint4 ring[];
+    // two rows': a bit per element of the row's vectors, set on slots
+    uint32_t *bitmaps = reinterpret_cast<uint32_t *>(ring + kStages * kChunk);
+    constexpr int P = kThreads + 32;  // walkers and slot warp
+    __shared__ RowSums buf[2][P / 32];
+    __shared__ Slots slots[2];
+    __shared__ RingCtl ctl;
+    const int tid = threadIdx.x;
+    const bool walker = tid < kThreads;
+    const int words = static_cast<int>((a.V + Vec<T>::N + 31) / 32);
+    for (int i = tid; i < 2 * words; i += kThreads + 64) bitmaps[i] = 0;
+    if (tid == 0) ring_init(ctl);
+    __syncthreads();
+    pdl_wait();
+    pdl_allow_dependents();
+    RingPos pos;
+    auto row_of = [&](const void *x, int64_t t) {
+        return Row<T>(const_cast<T *>(static_cast<const T *>(x)) + t * a.ld, static_cast<int>(a.V));
+    };
+    if (tid >= P) {
+        if (tid == P) {
+            for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+                if (a.weight && a.weight[t] == 0.0f) continue;
+                ring_fill(row_of(a.x, t), ring, ctl, pos, a.err);
+                if (a.dx) ring_fill(row_of(a.x, t), ring, ctl, pos, a.err);
+            }
+            ring_end(ctl);
         }
-        const double p = static_cast<double>(ex2((sl.x[i] - all.m) * a.c)) / all.S;
-        sl.grad[i] = static_cast<float>(up * (p - q));
+        return;
     }
-    if (lane == 0) {
-        // a teacher without an alternative, or a student without an entry: no loss
-        const bool zero = !bad_id && !tnan && ((!TAIL && !any) || all.S == 0.0f);
-        const bool nan = bad_id || tnan || !(all.S >= 0.0f);
-        const double F = static_cast<double>(ex2(fmaxf((s.m - all.m) * a.c, -1e4f)));
-        double coef = F / all.S;
-        if (live) coef -= qr / s.S;
-        sl.zero = zero;
-        sl.coef = nan ? NAN : static_cast<float>(up * coef);
-        if (loss) *loss = zero ? 0.0f : nan ? NAN : static_cast<float>(w * L);
+    int turn = 0;
+    RawSlots raw;
+    if (!walker) {
+        raw.fetch(a, blockIdx.x);
+        prepare_slots<T, TAIL>(a, blockIdx.x, raw, slots[0], bitmaps);
+        raw.fetch(a, static_cast<int64_t>(blockIdx.x) + gridDim.x);
+    }
+    bar<P>();
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
+        Slots &sl = slots[turn];
+        uint32_t *bitmap = bitmaps + turn * words;
+        const Row<T> row = row_of(a.x, t);
+        const Row<T> out = row_of(a.dx ? a.dx : a.x, t);  // same phase as the row
+        const float w = sl.w;
+        const bool skip = w == 0.0f;  // a token without a loss: nothing of its row is read
+        if (walker && !skip) {
+            Sums<false> mine(a.c);
+            // slots are left out of the sums
+            auto mask = [&](uint4 &r, int v) {
+                const int at = v * Vec<T>::N;
+                const uint32_t bits = (bitmap[at >> 5] >> (at & 31)) & ((1u << Vec<T>::N) - 1u);
+                if (bits) {
+#pragma unroll 1
+                    for (int j = 0; j < Vec<T>::N; ++j)
+                        if ((bits >> j) & 1u) Vec<T>::set(r, j, Vec<T>::kFill);
+                }
+            };
+            ring_walk(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int n) {
+                if (TAIL) {
+#pragma unroll
+                    for (int u = 0; u < kUnroll; ++u)
+                        if (u < n) mask(r[u], v + u * kThreads);
+                }
+                mine.template add<T, kUnroll>(r, a.c);
+            });
+            int ve;
+            if (row.edge(ve)) {
+                uint4 r[1] = {row.load_edge(ve)};
+                if (TAIL) mask(r[0], ve);
+                mine.template add<T, 1>(r, a.c);
+            }
+            const RowSums mine_w = warp_join(mine, a.c);
+            if ((tid & 31) == 0) buf[turn][tid >> 5] = mine_w;
+        } else if (!walker && t + gridDim.x < a.T) {
+            prepare_slots<T, TAIL>(a, t + gridDim.x, raw, slots[turn ^ 1], bitmaps + (turn ^ 1) * words);
+            raw.fetch(a, t + 2 * static_cast<int64_t>(gridDim.x));
+        }
+        bar<P>();
+        RowSums s;
+        RowState st;
+        if (!skip) {
+            s = warps_join<kWarps, false>(buf[turn], a.c);
+            if (is_far(s)) {
+                bar<P>();
+                s = far_sums<P>(row, a.c, buf[turn], [&](int e) {
+                    const int at = e + row.mis;
+                    return !TAIL || !((bitmap[at >> 5] >> (at & 31)) & 1u);
+                });
+            }
+            // without a gradient the walkers are done with the row: no barrier keeps its
+            // slots from the row after next
+            if (a.dx || !walker) st = row_state<TAIL>(a, sl, s);
+        }
+        if (walker) {
+            if (a.dx) {
+                if (skip) {
+                    zero_row(out);
+                } else {
+                    const uint64_t nm = f2_pack(-s.m, -s.m), c2 = f2_pack(a.c, a.c), k2 = f2_pack(st.coef, st.coef);
+                    auto grad = [&](const uint4 &r) {
+                        uint64_t e[Vec<T>::N / 2];
+                        Vec<T>::pairs(r, e);
+#pragma unroll
+                        for (int i = 0; i < Vec<T>::N / 2; ++i) {
+                            float lo, hi;
+                            f2_unpack(f2_mul(f2_add(e[i], nm), c2), lo, hi);
+                            e[i] = f2_mul(f2_pack(ex2(lo), ex2(hi)), k2);
+                        }
+                        return Vec<T>::from_pairs(e);
+                    };
+                    const bool zero = st.zero;
+                    ring_walk(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int n) {
+#pragma unroll
+                        for (int u = 0; u < kUnroll; ++u)
+                            if (u < n)
+                                __stcs(const_cast<uint4 *>(out.vec(v + u * kThreads)),
+                                       zero ? make_uint4(0, 0, 0, 0) : grad(r[u]));
+                    });
+                    int ve;
+                    if (row.edge(ve)) out.store_edge(ve, zero ? make_uint4(0, 0, 0, 0) : grad(row.load_edge(ve)));
+                }
+            }
+        } else if (skip) {
+            if (tid == kThreads && a.loss) a.loss[t] = 0.0f;
+        } else {
+            finish_slots<TAIL>(a, sl, s, st, t);
+        }
+        if (a.dx) bar<P>();  // the walkers' stores of the row are done
+        if (!walker && !skip) {
+            for (int i = tid & 31; i < a.k; i += 32)
+                if (sl.id[i] >= 0) {
+                    if (a.dx && !st.zero && sl.first[i]) Vec<T>::store(out.base + out.mis + sl.id[i], sl.x[i]);
+                    bitmap[(sl.id[i] + row.mis) >> 5] = 0;
+                }
+            __syncwarp();
+        }
     }
 }
 
-template <typename T, bool TAIL>
-__global__ void __launch_bounds__(kThreads, 4) k_distill(const DistillArgs a) {
-    extern __shared__ uint32_t bitmap[];  // one bit per element of the row's vectors: it is a slot
-    __shared__ RowSums buf[kWarps];
-    __shared__ Slots sl;
-    const int tid = threadIdx.x;
-    const int words = static_cast<int>((a.V + Vec<T>::N + 31) / 32);
-    for (int i = tid; i < words; i += kThreads) bitmap[i] = 0;
-    pdl_wait();
-    pdl_allow_dependents();
-    __syncthreads();
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
-        T *p = const_cast<T *>(static_cast<const T *>(a.x)) + t * a.ld;
-        const Row<T> row(p, a.V);
-        const Row<T> out(a.dx ? static_cast<T *>(a.dx) + t * a.ld : p, a.V);  // same phase as the row
-        const float w = a.weight ? a.weight[t] : 1.0f;
-        if (w == 0.0f) {  // a token without a loss: nothing of its row is read
-            if (a.dx)
-                for (int64_t v = tid; v < out.nv; v += kThreads) out.store(v, make_uint4(0, 0, 0, 0));
-            if (tid == 0 && a.loss) a.loss[t] = 0.0f;
-            continue;
-        }
-        bool bad = false, twice = false;
-        if (tid < a.k) {
-            const int64_t id = a.ids[t * a.k + tid];
-            bad = id >= a.V;
-            const bool use = id >= 0 && !bad;
-            sl.id[tid] = use ? static_cast<int>(id) : -1;
-            sl.first[tid] = false;
-            if (use) {
-                const int at = static_cast<int>(id + row.mis);
-                const uint32_t bit = 1u << (at & 31);
-                const bool first = !(atomicOr(&bitmap[at >> 5], bit) & bit);
-                sl.first[tid] = first;
-                twice = !first;
-                sl.x[tid] = Vec<T>::load(p + id);
-                sl.tl[tid] = a.tlp[t * a.k + tid];
-            }
-        }
-        bad = __syncthreads_or(bad);
-        twice = __syncthreads_or(twice);
-        Sums<false> mine;
-        for (int64_t v = tid; v < row.nv; v += kThreads * kUnroll) {
-            uint4 r[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int64_t vv = v + u * kThreads;
-                r[u] = vv < row.nv ? row.load(vv)
-                                   : make_uint4(Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill);
-            }
-            if (TAIL) {
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    const int64_t vv = v + u * kThreads;
-                    if (vv < row.nv) {
-                        const int at = static_cast<int>(vv * Vec<T>::N);
-                        const uint32_t bits = (bitmap[at >> 5] >> (at & 31)) & ((1u << Vec<T>::N) - 1u);
-                        if (bits)
-                            for (int j = 0; j < Vec<T>::N; ++j)
-                                if ((bits >> j) & 1u) Vec<T>::set(r[u], j, Vec<T>::kFill);
-                    }
-                }
-            }
-            mine.template add<T, kUnroll>(r, a.c);
-        }
-        const RowSums s = block_join(mine, a.c, buf);
-        if (tid < 32) finish_slots<TAIL>(a, sl, s, bad, twice, w, a.loss ? a.loss + t : nullptr);
-        __syncthreads();
-        if (a.dx) {
-            const float coef = sl.coef;
-            const bool zero = sl.zero;
-            const uint64_t nm = f2_pack(-s.m, -s.m), c2 = f2_pack(a.c, a.c), k2 = f2_pack(coef, coef);
-            for (int64_t v = tid; v < row.nv; v += kThreads * kUnroll) {
-                uint4 r[kUnroll];
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u)
-                    if (v + u * kThreads < row.nv) r[u] = row.load(v + u * kThreads);
-#pragma unroll
-                for (int u = 0; u < kUnroll; ++u) {
-                    if (v + u * kThreads >= row.nv) continue;
-                    uint64_t e[Vec<T>::N / 2];
-                    Vec<T>::pairs(r[u], e);
-#pragma unroll
-                    for (int i = 0; i < Vec<T>::N / 2; ++i) {
-                        float lo, hi;
-                        f2_unpack(f2_mul(f2_add(e[i], nm), c2), lo, hi);
-                        e[i] = f2_mul(f2_pack(ex2(lo), ex2(hi)), k2);
-                    }
-                    out.store(v + u * kThreads, zero ? make_uint4(0, 0, 0, 0) : Vec<T>::from_pairs(e));
-                }
-            }
-        }
-        __syncthreads();
-        if (tid < a.k && sl.id[tid] >= 0) {
-            if (a.dx && !sl.zero && !bad && sl.first[tid])
-                Vec<T>::store(out.base + out.mis + sl.id[tid], isnan(sl.coef) ? NAN : sl.grad[tid]);
-            bitmap[static_cast<int>(sl.id[tid] + row.mis) >> 5] = 0;
-        }
-        __syncthreads();
-    }
+// Shared memory beyond the default of a kernel: set once per device (setting it twice
+// from racing threads is harmless).
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t> &done, const DeviceInfo &dev) {
+    const uint64_t bit = 1ull << (dev.device & 63);
+    if (done.load() & bit) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess) done.fetch_or(bit);
+    return e;
 }
 
 }  // namespace
+
+template <typename T, bool TOP>
+static cudaError_t launch_logprobs_t(const LogprobArgs &a, const DeviceInfo &dev, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    auto kern = k_token_logprobs<T, TOP>;
+    cudaError_t e = allow_smem(kern, kRingBytes, done, dev);
+    if (e != cudaSuccess) return e;
+    const int grid = static_cast<int>(std::min<int64_t>(a.T, static_cast<int64_t>(dev.sm_count) * kCtasPerSm));
+    return launch_pdl(kern, dim3(grid), dim3(kThreads + 32), kRingBytes, st, a);
+}
 
 cudaError_t launch_token_logprobs(const void *x, bool f32, int64_t ld, int64_t T, int64_t V, const int64_t *targets,
                                   double temperature, int k, float *logprob, float *entropy, int64_t *top_ids,
                                   float *top_logprobs, const DeviceInfo &dev, cudaStream_t st) {
     LogprobArgs a{x, ld, T, V, targets, static_cast<float>(1.44269504088896340736 / temperature), 1.0 / temperature,
-                  k, logprob, entropy, top_ids, top_logprobs};
-    const int grid = static_cast<int>(std::min<int64_t>(T, static_cast<int64_t>(dev.sm_count) * 4));
-    return f32 ? launch_pdl(k_token_logprobs<float>, dim3(grid), dim3(kThreads), 0, st, a)
-               : launch_pdl(k_token_logprobs<__nv_bfloat16>, dim3(grid), dim3(kThreads), 0, st, a);
+                  k, logprob, entropy, top_ids, top_logprobs, device_error_word()};
+    if (!a.err) return cudaErrorInvalidSymbol;
+    if (f32) return k ? launch_logprobs_t<float, true>(a, dev, st) : launch_logprobs_t<float, false>(a, dev, st);
+    return k ? launch_logprobs_t<__nv_bfloat16, true>(a, dev, st) : launch_logprobs_t<__nv_bfloat16, false>(a, dev, st);
 }
 
 template <typename T, bool TAIL>
 static cudaError_t launch_distill_t(const DistillArgs &a, const DeviceInfo &dev, cudaStream_t st) {
-    const size_t smem = static_cast<size_t>((a.V + Vec<T>::N + 31) / 32) * 4;
-    cudaError_t e = cudaFuncSetAttribute(k_distill<T, TAIL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (kDistillMaxV + 64) / 8);
+    static std::atomic<uint64_t> done{0};
+    auto kern = k_distill<T, TAIL>;
+    cudaError_t e = allow_smem(kern, kRingBytes + static_cast<size_t>((kDistillMaxV + 64) / 4), done, dev);
     if (e != cudaSuccess) return e;
-    const int grid = static_cast<int>(std::min<int64_t>(a.T, static_cast<int64_t>(dev.sm_count) * 4));
-    return launch_pdl(k_distill<T, TAIL>, dim3(grid), dim3(kThreads), smem, st, a);
+    const size_t smem = kRingBytes + static_cast<size_t>((a.V + Vec<T>::N + 31) / 32) * 8;
+    // The rows that are walked twice at a time have to stay in the 126 MB L2 beside what
+    // is written.
+    const int64_t row_bytes = a.V * static_cast<int64_t>(sizeof(T)) * dev.sm_count;
+    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(kCtasPerSm, (80ll << 20) / std::max<int64_t>(row_bytes, 1)));
+    const int grid = static_cast<int>(std::min<int64_t>(a.T, dev.sm_count * per_sm));
+    return launch_pdl(kern, dim3(grid), dim3(kThreads + 64), smem, st, a);
 }
 
 cudaError_t launch_distill_topk(const void *x, bool f32, int64_t ld, int64_t T, int64_t V, const int64_t *ids,
                                 const float *tlp, int k, double temperature, bool tail, const float *weight,
                                 float *loss, void *dx, const DeviceInfo &dev, cudaStream_t st) {
     const DistillArgs a{x, ld, T, V, ids, tlp, k, static_cast<float>(1.44269504088896340736 / temperature),
-                        1.0 / temperature, weight, loss, dx};
+                        1.0 / temperature, weight, loss, dx, device_error_word()};
+    if (!a.err) return cudaErrorInvalidSymbol;
     if (f32) return tail ? launch_distill_t<float, true>(a, dev, st) : launch_distill_t<float, false>(a, dev, st);
     return tail ? launch_distill_t<__nv_bfloat16, true>(a, dev, st) : launch_distill_t<__nv_bfloat16, false>(a, dev, st);
 }
