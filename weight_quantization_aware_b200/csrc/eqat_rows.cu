@@ -44,7 +44,7 @@ constexpr int kStages = 3;                           // chunks of the ring
 constexpr size_t kRingBytes = static_cast<size_t>(kStages) * kChunk * 16;
 constexpr int kCtasPerSm = 3;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;     // far above any legitimate wait
-constexpr int kCandidates = 2048;  // vectors with candidates of the top-k selection, in shared memory
+constexpr int kNotes = 256;        // vectors that a warp notes for the top-k selection, in shared memory
 constexpr int kKept = 1024;        // entries among them that are ranked
 constexpr float kFloor = -1e30f;   // below every logit that has a part in its row
 constexpr uint32_t kNegInfBf16x2 = 0xFF80FF80u;
@@ -585,12 +585,12 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 struct TopShared {
-    int vecs[kCandidates];   // vectors with an entry that reached the walk's bound
+    int vecs[kWarps][kNotes];  // each warp's vectors with an entry that reached the walk's bound
     alignas(16) uint64_t kept[kKept];  // entries that reach the row's last bound: key << 32 | ~index
     uint32_t max_key[kThreads];
     double logS;
     float bound;
-    int count, kept_count;
+    int kept_count, overflow;
     int warp_count[kWarps];
 };
 
@@ -644,7 +644,7 @@ __device__ __noinline__ void top_k_by_bits(const Row<T> row, int k, TopShared &s
 
 // A value that at least k entries walked so far reach (-FLT_MAX while there are fewer):
 // the k-th largest of the threads' maxima, to its upper 16 bits, found by one warp with a
-// bisection on the counts, over the bits in which the maxima differ.
+// search on the counts, two bits a step, over the bits in which the maxima differ.
 __device__ __forceinline__ float refresh_bound(float thread_max, int k, TopShared &sh) {
     sh.max_key[threadIdx.x] = order_key(thread_max);
     bar<kThreads>();
@@ -658,16 +658,19 @@ __device__ __forceinline__ float refresh_bound(float thread_max, int k, TopShare
         }
         lo = __reduce_min_sync(0xffffffffu, lo);
         hi = __reduce_max_sync(0xffffffffu, hi);
-        const int top = 31 - __clz(static_cast<int>(lo ^ hi));  // the highest bit that differs; -1: none
-        uint32_t t = top < 31 ? hi & ~((2u << top) - 1u) : 0u;
-        if (top < 0) t = hi;
+        // two-bit digits at 30, 28, .. 16; above `top` all maxima agree
+        const int top = (31 - __clz(static_cast<int>((lo ^ hi) | 1u))) & ~1;
+        uint32_t t = top < 30 ? hi & ~((4u << top) - 1u) : 0u;
 #pragma unroll 1
-        for (int b = top; b >= 16; --b) {
-            const uint32_t cand = t | (1u << b);
-            uint32_t n = 0;
+        for (int b = top; b >= 16; b -= 2) {
+            uint32_t n = 0;  // how many reach digits 1, 2 and 3, ten bits each (at most 256 do)
 #pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i) n += q[i] >= cand;
-            if (__reduce_add_sync(0xffffffffu, n) >= static_cast<uint32_t>(k)) t = cand;
+            for (int i = 0; i < kThreads / 32; ++i)
+                n += (q[i] >= t + (1u << b) ? 1u : 0u) + (q[i] >= t + (2u << b) ? 1u << 10 : 0u) +
+                     (q[i] >= t + (3u << b) ? 1u << 20 : 0u);
+            n = __reduce_add_sync(0xffffffffu, n);
+            const uint32_t need = static_cast<uint32_t>(k);
+            t += ((n >> 20) >= need ? 3u : ((n >> 10) & 1023u) >= need ? 2u : (n & 1023u) >= need ? 1u : 0u) << b;
         }
         // a thread without an entry above kFloor says about kFloor: no bound then
         const float v = key_value(t);
@@ -677,25 +680,41 @@ __device__ __forceinline__ float refresh_bound(float thread_max, int k, TopShare
     return sh.bound;
 }
 
-// Notes vector v if one of its entries reaches the bound.
+// Notes vector v of the lanes where `hit`, in the warp's list; n is its length.
+__device__ __forceinline__ void note(bool hit, int v, int &n, TopShared &sh) {
+    const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+    if (hits) {
+        const int lane = threadIdx.x & 31, at = n + __popc(hits & ((1u << lane) - 1u));
+        if (hit && at < kNotes) sh.vecs[threadIdx.x >> 5][at] = v;
+        n += __popc(hits);
+    }
+}
+
+// Entries of vector v that reach the bound, to the kept ones.
 template <typename T>
-__device__ __forceinline__ void note(const uint4 &r, int v, float bound, TopShared &sh) {
-    if (Vec<T>::max(r) >= bound) {  // NaN and -inf never do
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < kCandidates) sh.vecs[at] = v;
+__device__ __forceinline__ void keep(const Row<T> &row, const uint4 &r, int v, float bound, TopShared &sh) {
+    uint32_t hits = 0;
+#pragma unroll
+    for (int j = 0; j < Vec<T>::N; ++j) hits |= Vec<T>::value(r, j) >= bound ? 1u << j : 0u;  // NaN and -inf never do
+    int at = hits ? atomicAdd(&sh.kept_count, __popc(hits)) : 0;
+    for (; hits; hits &= hits - 1, ++at) {
+        const int j = __ffs(static_cast<int>(hits)) - 1;
+        if (at < kKept) sh.kept[at] = (static_cast<uint64_t>(order_key(Vec<T>::value(r, j))) << 32) | ~row.index(v, j);
     }
 }
 
 // The walk for the sums, which also notes the vectors that may hold alternatives: those
-// with an entry that reaches a bound, refreshed each time the part walked has doubled.
-// For a row in random order these are about k log2(batches) vectors.
+// with an entry that reaches a bound, refreshed when 1, 4, 16, ... chunks are walked and
+// after the last.  For a row in random order these are about 4 k log4(chunks) vectors.
 template <typename T>
 __device__ __forceinline__ Sums<true> walk_candidates(const Row<T> &row, const LogprobArgs &a, const uint4 *ring,
-                                                      RingCtl &ctl, RingPos &pos, TopShared &sh) {
+                                                      RingCtl &ctl, RingPos &pos, TopShared &sh, int &notes) {
     Sums<true> s(a.c);
-    if (threadIdx.x == 0) sh.count = sh.kept_count = 0;
+    if (threadIdx.x == 0) sh.kept_count = sh.overflow = 0;
+    notes = 0;
     float bound = -FLT_MAX;
-    int ve, done = 0;
+    int ve, done = 0, next = 1;
+    const int chunks = chunks_of(row);
     const bool edge = row.edge(ve);
     if (edge) {
         uint4 r[1] = {row.load_edge(ve)};
@@ -703,15 +722,18 @@ __device__ __forceinline__ Sums<true> walk_candidates(const Row<T> &row, const L
     }
     ring_walk(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int) {
         const float mx = s.template add<T, kUnroll>(r, a.c);
-        if ((done & (done + 1)) == 0) bound = refresh_bound(s.m, a.k, sh);  // 1, 2, 4, ... chunks walked
-        ++done;
-        if (mx >= bound) {
+        if (++done == next) {
+            bound = refresh_bound(s.m, a.k, sh);
+            next = min(4 * next, chunks);
+        }
+        if (__any_sync(0xffffffffu, mx >= bound)) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) note<T>(r[u], v + u * kThreads, bound, sh);
+            for (int u = 0; u < kUnroll; ++u) note(Vec<T>::max(r[u]) >= bound, v + u * kThreads, notes, sh);
         }
     });
     if (done == 0) bound = refresh_bound(s.m, a.k, sh);  // a row within two vectors
-    if (edge) note<T>(row.load_edge(ve), ve, bound, sh);
+    note(edge, ve, notes, sh);
+    if (notes > kNotes) sh.overflow = 1;
     return s;
 }
 
@@ -719,36 +741,26 @@ __device__ __forceinline__ Sums<true> walk_candidates(const Row<T> &row, const L
 // vectors noted in its walk: their entries that reach the row's last bound are ranked by
 // counting.
 template <typename T>
-__device__ __forceinline__ void top_k(const Row<T> &row, const LogprobArgs &a, int64_t t, float thread_max, float m,
+__device__ __forceinline__ void top_k(const Row<T> &row, const LogprobArgs &a, int64_t t, float m, int notes,
                                       TopShared &sh) {
     const int tid = threadIdx.x, k = a.k;
-    const float bound = refresh_bound(thread_max, k, sh);  // its barriers also end the walk's notes
-    if (sh.count > kCandidates) {  // a row that rises along the walk: note again, by the last bound
-        bar<kThreads>();
-        if (tid == 0) sh.count = 0;
-        bar<kThreads>();
+    const float bound = sh.bound;  // the walk's last; the barrier of the sums ended its notes
+    if (sh.overflow) {  // a row that rises along the walk: walked again, by the last bound
         walk_body<kThreads, kUnroll>(row, [&](uint4(&r)[kUnroll], int v, int) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) note<T>(r[u], v + u * kThreads, bound, sh);
+            for (int u = 0; u < kUnroll; ++u)
+                if (Vec<T>::max(r[u]) >= bound) keep(row, r[u], v + u * kThreads, bound, sh);
         });
         int ve;
-        if (row.edge(ve)) note<T>(row.load_edge(ve), ve, bound, sh);
-        bar<kThreads>();
-    }
-    for (int i = tid; i < min(sh.count, kCandidates); i += kThreads) {
-        const int v = sh.vecs[i];
-        const uint4 r = v >= row.b0 && v < row.b1 ? load_vec(row.vec(v)) : row.load_edge(v);
-#pragma unroll
-        for (int j = 0; j < Vec<T>::N; ++j) {
-            const float x = Vec<T>::value(r, j);
-            if (x >= bound) {
-                const int at = atomicAdd(&sh.kept_count, 1);
-                if (at < kKept) sh.kept[at] = (static_cast<uint64_t>(order_key(x)) << 32) | ~row.index(v, j);
-            }
+        if (row.edge(ve)) keep(row, row.load_edge(ve), ve, bound, sh);
+    } else {
+        for (int i = tid & 31; i < notes; i += 32) {
+            const int v = sh.vecs[tid >> 5][i];
+            keep(row, v >= row.b0 && v < row.b1 ? load_vec(row.vec(v)) : row.load_edge(v), v, bound, sh);
         }
     }
     bar<kThreads>();
-    if (sh.count > kCandidates || sh.kept_count > kKept) top_k_by_bits(row, k, sh);
+    if (sh.kept_count > kKept) top_k_by_bits(row, k, sh);
     const int n = sh.kept_count;
     for (int i = tid; i < n; i += kThreads) {
         const uint64_t mine = sh.kept[i];
@@ -801,9 +813,10 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) k_token_logprobs(co
         float xt = 0.0f;
         if (id >= 0 && id < a.V) xt = Vec<T>::load(row.base + row.mis + id);
         if (threadIdx.x == 0 && t + gridDim.x < a.T) next_id = a.targets[t + gridDim.x];
+        int notes = 0;
         const Sums<true> mine = [&] {
             if constexpr (TOP) {
-                return walk_candidates(row, a, ring, ctl, pos, sh);
+                return walk_candidates(row, a, ring, ctl, pos, sh, notes);
             } else {
                 Sums<true> s(a.c);
                 ring_walk(row, ring, ctl, pos, a.err,
@@ -849,7 +862,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) k_token_logprobs(co
                     a.top_logprobs[t * a.k + i] = bad ? NAN : -INFINITY;
                 }
             } else {
-                top_k(row, a, t, mine.m, s.m, sh);
+                top_k(row, a, t, s.m, notes, sh);
             }
             bar<kThreads>();  // the next row's walk clears the counts
         }
