@@ -500,29 +500,52 @@ def fq_linear_fwd_mse(X, W, s, z, T, bits, group, ws=None, dY=None, loss=None):
 
 
 # ---------------------------------------------------------------- rows of logits
+#
+# The calls below are short on the device (a few microseconds at decode sizes), so their
+# checks are made in one pass per tensor that also returns the pointer.
 
 
-def _here(*ts):
-    """Refuses tensors that are not on the current CUDA device, whose stream the call
-    goes to."""
-    dev = torch.cuda.current_device()
-    for t in ts:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+def _arg(t, name, dtype, shape, dev):
+    """The pointer of a dense CUDA tensor of this dtype and shape on device `dev`."""
+    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous()
+            and t.get_device() == dev):
+        return t.data_ptr()
+    _shape(t, name, shape)
+    _req(t, name, dtype)
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _rows(x, name):
-    """(T, V, ld) of logits [T, V] whose rows are dense and ld elements apart."""
+def _opt(t, name, dtype, shape, dev):
+    return None if t is None else _arg(t, name, dtype, shape, dev)
+
+
+def _check(fn, st):
+    if st:
+        raise EqatError(fn, st, _lib.eqat_last_error_detail().decode())
+
+
+def _enter():
+    """(library, current device, raw handle of its current stream)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -1
+    return _lib or load_library(), dev, torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
+
+
+def _rows(x, name, dev):
+    """(T, V, row stride) of logits [T, V] whose rows are dense and do not overlap."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if x.dim() != 2:
         raise ValueError(f"{name} must be 2-D [T, V], got shape {tuple(x.shape)}")
     T, V = x.shape
-    ld = x.stride(0) if T > 1 else V
-    if (V > 1 and x.stride(1) != 1) or ld < V:
+    ld, sv = x.stride()
+    if T <= 1:
+        ld = V
+    if (V > 1 and sv != 1) or ld < V:
         raise ValueError(f"{name} must have dense rows that do not overlap, got strides {x.stride()}")
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if x.get_device() != dev:
+        raise ValueError(f"{name} is on {x.device}, the current device is cuda:{dev}")
     return T, V, ld
 
 
@@ -532,45 +555,46 @@ def token_logprobs(logits, targets, top_k=0, temperature=1.0):
     alternatives: returns (logprob [T], entropy [T], top_ids int64 [T, top_k],
     top_logprobs [T, top_k]), fp32 except the ids; the last two are None where top_k is
     0.  Equal logits rank by index; alternatives that a row lacks have id -1."""
-    _shape(targets, "targets", (logits.shape[0],))
-    T, V, ld = _rows(logits, "logits")
-    _req(targets, "targets", torch.int64)
-    _here(logits, targets)
-    f32 = dict(dtype=torch.float32, device=logits.device)
-    lp, ent = torch.empty(T, **f32), torch.empty(T, **f32)
+    lib, dev, stream = _enter()
+    T, V, ld = _rows(logits, "logits", dev)
+    tp = _arg(targets, "targets", torch.int64, (T,), dev)
+    where = logits.device
+    lp, ent = (torch.empty(T, dtype=torch.float32, device=where) for _ in range(2))
     ids = top = None
     if top_k > 0:
-        ids = torch.empty((T, top_k), dtype=torch.int64, device=logits.device)
-        top = torch.empty((T, top_k), **f32)
-    _call("eqat_token_logprobs", _p(logits), _dt(logits), ld, T, V, _p(targets), temperature, top_k, _p(lp),
-          _p(ent), _p(ids), _p(top), _stream())
+        ids = torch.empty((T, top_k), dtype=torch.int64, device=where)
+        top = torch.empty((T, top_k), dtype=torch.float32, device=where)
+    _check("eqat_token_logprobs", lib.eqat_token_logprobs(
+        logits.data_ptr(), _dt(logits), ld, T, V, tp, temperature, top_k, lp.data_ptr(), ent.data_ptr(),
+        ids.data_ptr() if top_k > 0 else None, top.data_ptr() if top_k > 0 else None, stream))
     return lp, ent, ids, top
 
 
 def _distill(logits, ids, tlp, weight, temperature, tail, want_loss, want_grad, dlogits):
+    lib, dev, stream = _enter()
+    T, V, ld = _rows(logits, "logits", dev)
     if ids.dim() != 2:
         raise ValueError(f"ids must be 2-D [T, k], got shape {tuple(ids.shape)}")
     k = ids.shape[1]
-    _shape(ids, "ids", (logits.shape[0], k))
-    _shape(tlp, "tlp", (logits.shape[0], k))
-    _shape(weight, "weight", (logits.shape[0],))
-    _shape(dlogits, "dlogits", logits.shape)
-    T, V, ld = _rows(logits, "logits")
-    _req(ids, "ids", torch.int64); _req(tlp, "tlp", torch.float32)
-    if weight is not None:
-        _req(weight, "weight", torch.float32)
+    ip, tp = _arg(ids, "ids", torch.int64, (T, k), dev), _arg(tlp, "tlp", torch.float32, (T, k), dev)
+    wp = _opt(weight, "weight", torch.float32, (T,), dev)
+    where = logits.device
+    gp = None
     if want_grad:
         if dlogits is None:
-            dlogits = torch.empty((T, ld), dtype=logits.dtype, device=logits.device)
+            dlogits = torch.empty((T, ld), dtype=logits.dtype, device=where)
             dlogits = dlogits if ld == V else dlogits[:, :V]
-        elif _rows(dlogits, "dlogits")[2] != ld:
-            raise ValueError("dlogits must have the strides of logits")
-        elif dlogits.dtype != logits.dtype:
-            raise TypeError(f"dlogits must be {logits.dtype}, got {dlogits.dtype}")
-    loss = torch.empty(T, dtype=torch.float32, device=logits.device) if want_loss else None
-    _here(logits, ids, tlp, weight, dlogits)
-    _call("eqat_distill_topk", _p(logits), _dt(logits), ld, T, V, _p(ids), _p(tlp), k, temperature,
-          EQAT_DISTILL_TAIL if tail else 0, _p(weight), _p(loss), _p(dlogits), _stream())
+        else:
+            _shape(dlogits, "dlogits", (T, V))
+            if _rows(dlogits, "dlogits", dev)[2] != ld:
+                raise ValueError("dlogits must have the strides of logits")
+            if dlogits.dtype != logits.dtype:
+                raise TypeError(f"dlogits must be {logits.dtype}, got {dlogits.dtype}")
+        gp = dlogits.data_ptr()
+    loss = torch.empty(T, dtype=torch.float32, device=where) if want_loss else None
+    _check("eqat_distill_topk", lib.eqat_distill_topk(
+        logits.data_ptr(), _dt(logits), ld, T, V, ip, tp, k, temperature, EQAT_DISTILL_TAIL if tail else 0, wp,
+        loss.data_ptr() if want_loss else None, gp, stream))
     return loss, dlogits
 
 
@@ -600,18 +624,13 @@ def distill_topk_step(logits, ids, tlp, weight=None, temperature=1.0, tail=False
 # ---------------------------------------------------------------- microscaled 4-bit floats
 
 FP4_BLOCK = {"mx": 32, "nv": 16}
+_FP4_FMT = {"mx": 0, "nv": 1}
 
 
 def _fmt(fmt):
-    if fmt not in FP4_BLOCK:
+    if fmt not in _FP4_FMT:
         raise ValueError(f"fmt must be 'mx' or 'nv', got {fmt!r}")
-    return 1 if fmt == "nv" else 0
-
-
-def _tscale(g, name="tscale"):
-    if g is not None:
-        _shape(g, name, (1,))
-        _req(g, name, torch.float32)
+    return _FP4_FMT[fmt]
 
 
 def fp4_scale_shape(N: int, K: int, fmt: str):
@@ -620,6 +639,8 @@ def fp4_scale_shape(N: int, K: int, fmt: str):
 
 
 def _fp4_matrix(W, name="W"):
+    if not isinstance(W, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
     if W.dim() != 2:
         raise ValueError(f"{name} must be 2-D, got shape {tuple(W.shape)}")
     if W.shape[1] % 32:
@@ -627,15 +648,20 @@ def _fp4_matrix(W, name="W"):
     return W.shape
 
 
+def _codes_matrix(codes):
+    if codes.dim() != 2:
+        raise ValueError(f"codes must be 2-D [N, K/2], got shape {tuple(codes.shape)}")
+    return codes.shape[0], codes.shape[1] * 2
+
+
 def fp4_tensor_scale(W, out=None):
     """The tensor scale of the "nv" format: the smallest power of two g with
     max|W| <= 6 * 448 * g, one fp32 value on the device."""
-    _fp4_matrix(W)
-    _shape(out, "out", (1,))
-    _req(W, "W")
-    out = torch.empty(1, dtype=torch.float32, device=W.device) if out is None else _req(out, "out", torch.float32)
-    _here(W, out)
-    _call("eqat_fp4_tensor_scale", _p(W), _dt(W), W.numel(), _p(out), _stream())
+    lib, dev, stream = _enter()
+    wp = _arg(W, "W", W.dtype, _fp4_matrix(W), dev)
+    out = torch.empty(1, dtype=torch.float32, device=W.device) if out is None else out
+    _check("eqat_fp4_tensor_scale", lib.eqat_fp4_tensor_scale(
+        wp, _dt(W), W.numel(), _arg(out, "out", torch.float32, (1,), dev), stream))
     return out
 
 
@@ -643,44 +669,49 @@ def pack_fp4(W, fmt, tscale=None, codes=None, scales=None):
     """Packs W [N, K] (bf16 or fp32) into 4-bit floats: returns (codes uint8 [N, K/2],
     scales uint8 tiles of fp4_scale_shape(N, K, fmt)).  tscale: the tensor scale of "nv"."""
     f = _fmt(fmt)
+    lib, dev, stream = _enter()
     N, K = _fp4_matrix(W)
-    _shape(codes, "codes", (N, K // 2)); _shape(scales, "scales", fp4_scale_shape(N, K, fmt))
-    _req(W, "W")
-    _tscale(tscale)
-    codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device) if codes is None else \
-        _req(codes, "codes", torch.uint8)
-    scales = torch.empty(fp4_scale_shape(N, K, fmt), dtype=torch.uint8, device=W.device) if scales is None else \
-        _req(scales, "scales", torch.uint8)
-    _here(W, tscale, codes, scales)
-    _call("eqat_pack_fp4", _p(W), _dt(W), N, K, f, _p(tscale), _p(codes), _p(scales), _stream())
+    sshape = fp4_scale_shape(N, K, fmt)
+    if codes is not None:
+        _arg(codes, "codes", torch.uint8, (N, K // 2), dev)
+    if scales is not None:
+        _arg(scales, "scales", torch.uint8, sshape, dev)
+    wp, gp = _arg(W, "W", W.dtype, (N, K), dev), _opt(tscale, "tscale", torch.float32, (1,), dev)
+    if codes is None:
+        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
+    if scales is None:
+        scales = torch.empty(sshape, dtype=torch.uint8, device=W.device)
+    _check("eqat_pack_fp4", lib.eqat_pack_fp4(wp, _dt(W), N, K, f, gp, codes.data_ptr(), scales.data_ptr(), stream))
     return codes, scales
 
 
 def fake_quant_fp4(W, fmt, tscale=None, W_hat=None):
     """The values that pack_fp4 would store, in W's dtype."""
     f = _fmt(fmt)
+    lib, dev, stream = _enter()
     N, K = _fp4_matrix(W)
-    _shape(W_hat, "W_hat", (N, K))
-    _req(W, "W")
-    _tscale(tscale)
-    W_hat = torch.empty_like(W) if W_hat is None else _req(W_hat, "W_hat", W.dtype)
-    _here(W, tscale, W_hat)
-    _call("eqat_fake_quant_fp4", _p(W), _dt(W), N, K, f, _p(tscale), _p(W_hat), _stream())
+    wp, gp = _arg(W, "W", W.dtype, (N, K), dev), _opt(tscale, "tscale", torch.float32, (1,), dev)
+    if W_hat is None:
+        W_hat = torch.empty_like(W)
+        hp = W_hat.data_ptr()
+    else:
+        hp = _arg(W_hat, "W_hat", W.dtype, (N, K), dev)
+    _check("eqat_fake_quant_fp4", lib.eqat_fake_quant_fp4(wp, _dt(W), N, K, f, gp, hp, stream))
     return W_hat
 
 
 def dequant_fp4(codes, scales, fmt, tscale=None, dtype=torch.bfloat16, out=None):
     """The values of packed codes [N, K/2], [N, K] of `dtype` (or into `out`)."""
     f = _fmt(fmt)
-    if codes.dim() != 2:
-        raise ValueError(f"codes must be 2-D [N, K/2], got shape {tuple(codes.shape)}")
-    N, K = codes.shape[0], codes.shape[1] * 2
-    _shape(scales, "scales", fp4_scale_shape(N, K, fmt)); _shape(out, "out", (N, K))
-    _req(codes, "codes", torch.uint8); _req(scales, "scales", torch.uint8)
-    _tscale(tscale)
-    out = torch.empty((N, K), dtype=dtype, device=codes.device) if out is None else _req(out, "out")
-    _here(codes, scales, tscale, out)
-    _call("eqat_dequant_fp4", _p(codes), _p(scales), N, K, f, _p(tscale), _p(out), _dt(out), _stream())
+    lib, dev, stream = _enter()
+    N, K = _codes_matrix(codes)
+    cp = _arg(codes, "codes", torch.uint8, (N, K // 2), dev)
+    sp = _arg(scales, "scales", torch.uint8, fp4_scale_shape(N, K, fmt), dev)
+    gp = _opt(tscale, "tscale", torch.float32, (1,), dev)
+    if out is None:
+        out = torch.empty((N, K), dtype=dtype, device=codes.device)
+    op = _arg(out, "out", out.dtype, (N, K), dev)
+    _check("eqat_dequant_fp4", lib.eqat_dequant_fp4(cp, sp, N, K, f, gp, op, _dt(out), stream))
     return out
 
 
@@ -690,31 +721,35 @@ def fp4_workspace(M, N, K, fmt, backward=False, device=None) -> torch.Tensor:
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device or "cuda")
 
 
-def _fp4_linear(X, codes, scales, fmt, tscale, x_tscale, **mn):
-    f = _fmt(fmt)
+def _fp4_operands(X, codes, scales, fmt, tscale, x_tscale, dev):
     M, K = _fp4_matrix(X, "X")
-    if codes.dim() != 2:
-        raise ValueError(f"codes must be 2-D [N, K/2], got shape {tuple(codes.shape)}")
-    N = codes.shape[0]
-    _shape(codes, "codes", (N, K // 2)); _shape(scales, "scales", fp4_scale_shape(N, K, fmt))
-    for name, (t, shape) in mn.items():
-        _shape(t, name, {"MN": (M, N), "MK": (M, K), "NK": (N, K)}[shape])
-        if t is not None:
-            _req(t, name, torch.bfloat16)
-    _req(X, "X", torch.bfloat16); _req(codes, "codes", torch.uint8); _req(scales, "scales", torch.uint8)
-    _tscale(tscale); _tscale(x_tscale, "x_tscale")
-    return f, M, N, K
+    N, _ = _codes_matrix(codes)
+    return (M, N, K, _arg(X, "X", torch.bfloat16, (M, K), dev),
+            _arg(codes, "codes", torch.uint8, (N, K // 2), dev),
+            _arg(scales, "scales", torch.uint8, fp4_scale_shape(N, K, fmt), dev),
+            _opt(tscale, "tscale", torch.float32, (1,), dev), _opt(x_tscale, "x_tscale", torch.float32, (1,), dev))
+
+
+def _fp4_ws(ws, M, N, K, fmt, backward, dev, like):
+    if ws is None:
+        ws = fp4_workspace(M, N, K, fmt, backward, like.device)
+        return ws, ws.data_ptr(), ws.numel()
+    return ws, _arg(ws, "ws", torch.uint8, ws.shape, dev), ws.numel()
 
 
 def fp4_linear_fwd(X, codes, scales, fmt, tscale=None, x_tscale=None, ws=None, Y=None):
     """Y = X_hat W_hat^T with both operands in 4-bit floats: X [M, K] bf16 is packed in
     the call (tensor scale x_tscale), W comes from pack_fp4 (tensor scale tscale)."""
-    f, M, N, K = _fp4_linear(X, codes, scales, fmt, tscale, x_tscale, Y=(Y, "MN"))
-    Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device) if Y is None else Y
-    ws = fp4_workspace(M, N, K, fmt, False, X.device) if ws is None else _req(ws, "ws", torch.uint8)
-    _here(X, codes, scales, tscale, x_tscale, ws, Y)
-    _call("eqat_fp4_linear_fwd", _p(X), _p(codes), _p(scales), f, _p(x_tscale), _p(tscale), _p(Y), M, N, K,
-          _p(ws), ws.numel(), _stream())
+    f = _fmt(fmt)
+    lib, dev, stream = _enter()
+    M, N, K, xp, cp, sp, gw, gx = _fp4_operands(X, codes, scales, fmt, tscale, x_tscale, dev)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+        yp = Y.data_ptr()
+    else:
+        yp = _arg(Y, "Y", torch.bfloat16, (M, N), dev)
+    ws, wp, wn = _fp4_ws(ws, M, N, K, fmt, False, dev, X)
+    _check("eqat_fp4_linear_fwd", lib.eqat_fp4_linear_fwd(xp, cp, sp, f, gx, gw, yp, M, N, K, wp, wn, stream))
     return Y
 
 
@@ -722,15 +757,19 @@ def fp4_linear_bwd(X, codes, scales, dY, fmt, tscale=None, x_tscale=None, need_d
                    out=None):
     """Straight-through backward of fp4_linear_fwd: returns (dX = dY W_hat,
     dW = dY^T X_hat), None where not requested."""
-    dX, dW = (None, None) if out is None else out
-    f, M, N, K = _fp4_linear(X, codes, scales, fmt, tscale, x_tscale, dY=(dY, "MN"), dX=(dX, "MK"), dW=(dW, "NK"))
+    f = _fmt(fmt)
+    lib, dev, stream = _enter()
+    M, N, K, xp, cp, sp, gw, gx = _fp4_operands(X, codes, scales, fmt, tscale, x_tscale, dev)
+    dyp = _arg(dY, "dY", torch.bfloat16, (M, N), dev)
     if out is None:
         dX = torch.empty((M, K), dtype=torch.bfloat16, device=X.device) if need_dx else None
         dW = torch.empty((N, K), dtype=torch.bfloat16, device=X.device) if need_dw else None
-    ws = fp4_workspace(M, N, K, fmt, True, X.device) if ws is None else _req(ws, "ws", torch.uint8)
-    _here(X, codes, scales, tscale, x_tscale, dY, dX, dW, ws)
-    _call("eqat_fp4_linear_bwd", _p(X), _p(codes), _p(scales), f, _p(x_tscale), _p(tscale), _p(dY), _p(dX), _p(dW),
-          M, N, K, _p(ws), ws.numel(), _stream())
+    else:
+        dX, dW = out
+    ws, wp, wn = _fp4_ws(ws, M, N, K, fmt, True, dev, X)
+    _check("eqat_fp4_linear_bwd", lib.eqat_fp4_linear_bwd(
+        xp, cp, sp, f, gx, gw, dyp, _opt(dX, "dX", torch.bfloat16, (M, K), dev),
+        _opt(dW, "dW", torch.bfloat16, (N, K), dev), M, N, K, wp, wn, stream))
     return dX, dW
 
 

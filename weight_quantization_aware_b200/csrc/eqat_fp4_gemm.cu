@@ -304,6 +304,305 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
+// ---------------------------------------------------------------------------- CTA pairs
+// Many tokens: persistent pairs of SMs (cta_group::2).  A pair makes 256 x 256 tiles: each
+// CTA stages its 128 rows of A and 128 of B's 256 (with the scales of its rows of A and of
+// all of B's), the even CTA issues the MMAs, and each CTA's tensor memory holds its 128
+// accumulator rows.  Per SM that reads 64 bytes of operands a clock from shared memory
+// where a 128 x 256 tile of one CTA reads 96, and two thirds of its bytes from L2.
+//
+// Tensor memory has 512 columns: two accumulators of 256 would leave none for the scales.
+// So the accumulators of consecutive tiles start at columns 0 and 160 and overlap in 96;
+// the epilogue drains those first and lets the next tile's MMAs start while it drains the
+// other 160.  The last 96 columns hold the scales of two stages; before a stage's scales
+// are copied, the MMAs of the stage two before it have completed (its ring slot's barrier).
+constexpr int kPairThreads = 256;  // producer, issuer, allocator, one idle, four epilogue warps
+constexpr int kAcc1 = 160;         // first column of odd tiles' accumulators
+constexpr int kOverlap = 256 - kAcc1;
+constexpr int kScaleCols = 48;     // of one stage: 16 of A, 32 of B
+constexpr int kScaleBase = 512 - 2 * kScaleCols;
+static_assert(kAcc1 + 256 <= kScaleBase && kOverlap % 32 == 0, "tensor memory layout");
+
+template <bool NV>
+struct PairCfg {
+    static constexpr int SF = NV ? 4 : 2;
+    static constexpr int KSF = NV ? 64 : 128;
+    static constexpr int SF_BYTES = SF * kSfTile;  // of 128 rows
+    static constexpr int STAGE = 2 * kATile + 3 * SF_BYTES;
+    static constexpr int STAGES = 5;
+    static constexpr int OUT = 4 * 2 * 2048;  // two 32 x 32 bf16 chunks per epilogue warp
+    static constexpr int SMEM = 1024 + STAGES * STAGE + OUT + 256;
+    static_assert(STAGE % 1024 == 0 && SMEM <= 232448, "shared memory");
+};
+
+struct PairCtl {
+    uint64_t full[5], empty[5], acc_full, acc_free, drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(PairCtl) <= 256, "control block exceeds its slot");
+
+struct PairArgs {
+    int64_t sf_tiles_k;
+    int K, tiles_m, tiles;
+    int64_t rows_a, rows_b;
+    const float *ga, *gb;
+    int *err;
+    uint64_t wait_limit_ns;
+};
+
+__device__ __forceinline__ void tmem_cp_scales_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+template <bool NV>
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t accumulate) {
+    if (NV)
+        asm volatile(
+            "{\n"
+            ".reg .pred p;\n"
+            "setp.ne.b32 p, %6, 0;\n"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n"
+            "}\n" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n"
+            ".reg .pred p;\n"
+            "setp.ne.b32 p, %6, 0;\n"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n"
+            "}\n" ::"r"(d),
+            "l"(ad), "l"(bd), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// M = 256 in the instruction descriptor.
+__device__ constexpr uint32_t idesc_fp4_pair(bool nv, uint32_t sf_id) {
+    return (idesc_fp4(256, nv, sf_id) & ~(3u << 27)) | (2u << 27);
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *smem_src, int32_t c0, int32_t c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(smem_u32(smem_src)), "r"(c0), "r"(c1)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+template <bool NV>
+__global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
+    k_gemm2_fp4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                const __grid_constant__ CUtensorMap tmY, const PairArgs p) {
+    using C = PairCfg<NV>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    uint8_t *out = smem + C::STAGES * C::STAGE;
+    PairCtl *ctl = reinterpret_cast<PairCtl *>(out + C::OUT);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(&ctl->full[i], 1);
+            mbar_init(&ctl->empty[i], 1);
+        }
+        mbar_init(&ctl->acc_full, 1);
+        mbar_init(&ctl->acc_free, 8);  // four epilogue warps of each CTA
+        mbar_init(&ctl->drain, 1);
+        ctl->abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmSA);
+        tma_prefetch_desc(&tmSB);
+        tma_prefetch_desc(&tmY);
+    }
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_allow_dependents();
+    if (warp == 2) {
+        tmem_alloc_pair(&ctl->tmem_base, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    volatile int *abort_flag = &ctl->abort_flag;
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int nkb = (p.K + kKStage - 1) / kKStage;
+    const uint32_t full0 = map_to_rank(&ctl->full[0], 0);
+    const uint32_t acc_free0 = map_to_rank(&ctl->acc_free, 0);
+
+    if (warp == 0) {
+        // ---------------------------------------------------------- TMA producer (both CTAs)
+        if (elect_one_sync()) {
+            uint32_t it = 0, armed = 0, armed_parity = 0;
+            bool ok = true;
+            for (int t = pair; ok && t < p.tiles; t += npairs) {
+                const int tm = t % p.tiles_m, tn = t / p.tiles_m;
+                const int ra = tm * 2 + static_cast<int>(rank);  // 128-row tile of A
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    const int st = it % C::STAGES;
+                    const uint32_t ph = (it / C::STAGES) & 1u;
+                    if (!mbar_wait_bounded(&ctl->empty[st], ph ^ 1u, abort_flag, p.err, p.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *sa = smem + st * C::STAGE, *sb = sa + kATile, *sfa = sb + kATile, *sfb = sfa + C::SF_BYTES;
+                    if (leader) {
+                        mbar_arrive_expect_tx(&ctl->full[st], 2 * C::STAGE);
+                        armed |= 1u << st;
+                        armed_parity = (armed_parity & ~(1u << st)) | (ph << st);
+                    }
+                    const uint32_t bar = full0 + 8u * static_cast<uint32_t>(st);
+                    tma_load_2d_pair(sa, &tmA, bar, kb * 128, ra * 128);
+                    tma_load_2d_pair(sb, &tmB, bar, kb * 128, tn * 256 + static_cast<int>(rank) * 128);
+                    // scale tiles are numbered along K, then along the rows; what a box takes
+                    // past the end of K belongs to other rows and is not used
+                    const int sf = kb * C::SF;
+                    tma_load_2d_pair(sfa, &tmSA, bar, 0, static_cast<int>(ra * p.sf_tiles_k) + sf);
+                    tma_load_2d_pair(sfb, &tmSB, bar, 0, static_cast<int>(2 * tn * p.sf_tiles_k) + sf);
+                    tma_load_2d_pair(sfb + C::SF_BYTES, &tmSB, bar, 0, static_cast<int>((2 * tn + 1) * p.sf_tiles_k) + sf);
+                }
+            }
+            if (!ok) {
+                // Copies this CTA issued for stages the leader has not armed count on no
+                // phase that can complete: give them a fixed 2 ms to land.
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 2000000ull) {
+                }
+                if (leader)
+                    for (int st = 0; st < C::STAGES; ++st)
+                        if (armed & (1u << st)) {
+                            const uint32_t a = smem_u32(&ctl->full[st]);
+                            const uint64_t t1 = globaltimer_ns();
+                            while (!mbar_try_wait(a, (armed_parity >> st) & 1u) && globaltimer_ns() - t1 < 100000000ull) {
+                            }
+                        }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- MMA issuer (the leader)
+        if (leader && elect_one_sync()) {
+            uint32_t it = 0, local = 0;
+            bool ok = true, issued = false;
+            for (int t = pair; ok && t < p.tiles; t += npairs, ++local) {
+                // the previous tile's overlapping columns have been drained
+                if (local > 0 && !mbar_wait_bounded(&ctl->acc_free, (local - 1) & 1u, abort_flag, p.err, p.wait_limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + ((local & 1u) ? kAcc1 : 0);
+                for (int kb = 0; kb < nkb; ++kb, ++it) {
+                    const int st = it % C::STAGES;
+                    const uint32_t ph = (it / C::STAGES) & 1u;
+                    if (!mbar_wait_bounded(&ctl->full[st], ph, abort_flag, p.err, p.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    if (it >= 2) {  // the MMAs that read this scale buffer before
+                        const uint32_t o = it - 2;
+                        if (!mbar_wait_bounded(&ctl->empty[o % C::STAGES], (o / C::STAGES) & 1u, abort_flag, p.err,
+                                               p.wait_limit_ns)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(smem + st * C::STAGE), sb = sa + kATile, ssfa = sb + kATile,
+                                   ssfb = ssfa + C::SF_BYTES;
+                    const uint32_t tsf = tmem + kScaleBase + (it & 1u) * kScaleCols, tsfb = tsf + 16;
+                    const int kleft = p.K - kb * kKStage;
+                    const int nsf = kleft >= kKStage ? C::SF : (kleft + C::KSF - 1) / C::KSF;
+                    for (int j = 0; j < nsf; ++j) {
+                        tmem_cp_scales_pair(tsf + j * 4, smem_desc_plain(ssfa + j * kSfTile));
+                        tmem_cp_scales_pair(tsfb + j * 8, smem_desc_plain(ssfb + j * kSfTile));
+                        tmem_cp_scales_pair(tsfb + j * 8 + 4, smem_desc_plain(ssfb + C::SF_BYTES + j * kSfTile));
+                    }
+                    const int nmma = kleft >= kKStage ? kKStage / 64 : (kleft + 63) / 64;
+                    for (int kk = 0; kk < nmma; ++kk) {
+                        const uint64_t ad = smem_desc_sw128(sa + kk * 32, 16, 1024);
+                        const uint64_t bd = smem_desc_sw128(sb + kk * 32, 16, 1024);
+                        const int j = NV ? kk : kk >> 1;
+                        mma_fp4_pair<NV>(d, ad, bd, idesc_fp4_pair(NV, NV ? 0u : (kk & 1) * 2u), tsf + j * 4, tsfb + j * 8,
+                                         (kb > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    issued = true;
+                    tc_commit_pair(&ctl->empty[st], 3);
+                }
+                if (ok) tc_commit_pair(&ctl->acc_full, 3);
+            }
+            if (!ok && issued) {  // wait for the MMAs already issued before tensor memory is freed
+                tc_commit_pair(&ctl->drain, 1);
+                const uint32_t a = smem_u32(&ctl->drain);
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < 100000000ull) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        // ---------------------------------------------------------- epilogue (both CTAs)
+        const int quad = warp & 3;
+        uint8_t *buf = out + quad * 4096;
+        const float alpha = (p.ga ? __ldg(p.ga) : 1.0f) * (p.gb ? __ldg(p.gb) : 1.0f);
+        uint32_t local = 0, chunk = 0;
+        for (int t = pair; t < p.tiles; t += npairs, ++local) {
+            const bool ok = mbar_wait_bounded(&ctl->acc_full, local & 1u, abort_flag, p.err, p.wait_limit_ns);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            const int tm = t % p.tiles_m, tn = t / p.tiles_m;
+            const int row0 = tm * 256 + static_cast<int>(rank) * 128 + quad * 32;
+            const bool odd = local & 1u;
+            const uint32_t taddr = tmem + ((quad * 32) << 16) + (odd ? kAcc1 : 0);
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i, ++chunk) {
+                // the columns that the next tile's accumulator overlaps come first
+                const int c0 = 32 * (odd ? i : (i + kAcc1 / 32) & 7);
+                float v[32];
+                tmem_ld_32cols(taddr + c0, v);
+                if (i == kOverlap / 32 - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(acc_free0);
+                }
+                // 32 rows of 64 bytes, 16-byte units swizzled as the output map's box
+                uint8_t *dst = buf + (chunk & 1) * 2048;
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = pack_bf16x2(__fmul_rn(v[8 * q + 2 * j], alpha), __fmul_rn(v[8 * q + 2 * j + 1], alpha));
+                    *reinterpret_cast<uint4 *>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                // the map clips a chunk at the matrix's end
+                if (lane == 0 && row0 < p.rows_a && tn * 256 + c0 < p.rows_b) tma_store_2d(&tmY, dst, tn * 256 + c0, row0);
+            }
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while the pair's MMAs may still read its shared memory
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
 struct Side {
     const uint8_t *codes, *scales;
     const float *g;
@@ -350,13 +649,60 @@ cudaError_t launch_t(const Side &a, const Side &b, int64_t K, void *Y, int64_t l
 }
 
 template <bool NV>
+cudaError_t launch_pair(const Side &a, const Side &b, int64_t K, void *Y, const DeviceInfo &dev, cudaStream_t st) {
+    using C = PairCfg<NV>;
+    const int64_t tiles_k = (K / (NV ? 16 : 32) + 3) / 4;
+    CUtensorMap ma, mb, sa, sb, my;
+    auto codes = [&](CUtensorMap &m, const Side &s) {
+        return encode_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, s.codes, K / 2, s.rows, K / 2, 128, 128,
+                             CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    auto scales = [&](CUtensorMap &m, const Side &s) {  // one scale tile per row of the map
+        return encode_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, s.scales, kSfTile / 4, (s.rows + 127) / 128 * tiles_k,
+                             kSfTile, kSfTile / 4, C::SF, CU_TENSOR_MAP_SWIZZLE_NONE);
+    };
+    cudaError_t e;
+    if ((e = codes(ma, a)) != cudaSuccess || (e = codes(mb, b)) != cudaSuccess || (e = scales(sa, a)) != cudaSuccess ||
+        (e = scales(sb, b)) != cudaSuccess ||
+        (e = encode_map_2d(my, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, Y, b.rows, a.rows, b.rows * 2, 32, 32,
+                           CU_TENSOR_MAP_SWIZZLE_64B)) != cudaSuccess)
+        return e;
+    auto kern = k_gemm2_fp4<NV>;
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << (dev.device & 63);
+    if (!(done.load() & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit);
+    }
+    PairArgs p{};
+    p.sf_tiles_k = tiles_k;
+    p.K = static_cast<int>(K);
+    p.tiles_m = static_cast<int>((a.rows + 255) / 256);
+    const int64_t tiles = p.tiles_m * ((b.rows + 255) / 256);
+    // scale tiles are numbered in 32 bits
+    if (tiles > 0x7FFFFFFF || ((std::max(a.rows, b.rows) + 255) / 256 * 2 + 1) * tiles_k > 0x7FFFFFFF)
+        return cudaErrorInvalidValue;
+    p.tiles = static_cast<int>(tiles);
+    p.rows_a = a.rows;
+    p.rows_b = b.rows;
+    p.ga = a.g;
+    p.gb = b.g;
+    p.err = device_error_word();
+    if (!p.err) return cudaErrorInvalidSymbol;
+    p.wait_limit_ns = kWaitLimitNs;
+    const int grid = 2 * static_cast<int>(std::min<int64_t>(tiles, dev.sm_count / 2));
+    return launch_pdl(kern, dim3(grid), dim3(kPairThreads), C::SMEM, st, ma, mb, sa, sb, my, p);
+}
+
+template <bool NV>
 cudaError_t dispatch(const Side &x, const Side &w, int64_t K, void *Y, const DeviceInfo &dev, cudaStream_t st) {
     const int64_t M = x.rows, N = w.rows;
     if (M <= 16) return launch_t<16, NV, true>(w, x, K, Y, N, dev, st);
     if (M <= 32) return launch_t<32, NV, true>(w, x, K, Y, N, dev, st);
     if (M <= 64) return launch_t<64, NV, true>(w, x, K, Y, N, dev, st);
     if (M <= 128) return launch_t<128, NV, true>(w, x, K, Y, N, dev, st);
-    return launch_t<256, NV, false>(x, w, K, Y, N, dev, st);
+    return launch_pair<NV>(x, w, K, Y, dev, st);
 }
 
 }  // namespace
