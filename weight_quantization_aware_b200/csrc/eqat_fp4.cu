@@ -29,18 +29,47 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Two values -> two codes in a byte (the first in the low half): round to nearest even
-// on the e2m1 grid, saturating.
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+// Eight values -> eight codes (the first in the low half of the first byte): round to
+// nearest even on the e2m1 grid, saturating.
+__device__ __forceinline__ uint32_t e2m1x8(const float (&x)[16], int o) {
     uint32_t r;
     asm("{\n"
-        ".reg .b8 b;\n"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n"
-        "cvt.u32.u8 %0, b;\n"
+        ".reg .b8 b0, b1, b2, b3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+        "mov.b32 %0, {b0, b1, b2, b3};\n"
         "}\n"
         : "=r"(r)
-        : "f"(lo), "f"(hi));
+        : "f"(x[o]), "f"(x[o + 1]), "f"(x[o + 2]), "f"(x[o + 3]), "f"(x[o + 4]), "f"(x[o + 5]), "f"(x[o + 6]),
+          "f"(x[o + 7]));
     return r;
+}
+
+// Packed fp32 pairs: each lane is the IEEE operation.
+__device__ __forceinline__ uint64_t f2_pack(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float &lo, float &hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ float max_nan_abs(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
+    return d;
 }
 
 // x -> e4m3 byte, round to nearest even, 448 beyond it (x >= 0, not NaN).
@@ -61,12 +90,68 @@ __device__ __forceinline__ float e8m0_value(uint32_t b) {
     return b ? __uint_as_float(b << 23) : 0x1p-127f;
 }
 
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    // bf16 images of 0, .5, 1, 1.5, 2, 3, 4, 6, one byte each (the low bytes are 0x00,
-    // 0x80 or 0xC0): looked up in two registers
-    const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, c & 7u) & 0xFFu;
-    const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, c & 7u) & 0xFFu;
-    return __uint_as_float(((c & 8u) << 28) | (hi << 24) | (lo << 16));
+// Eight codes -> eight bf16 pairs-wise in four words.  The bf16 images of 0, .5, 1, 1.5,
+// 2, 3, 4, 6 are two tables of bytes; a byte permute looks up four codes at a time, since
+// the magnitudes are its selectors.
+__device__ __forceinline__ void e2m1_bf16x8(uint32_t c, uint32_t (&w)[4]) {
+    const uint32_t mag = c & 0x77777777u;
+    const uint32_t even = (c << 4) & 0x80808080u, odd = c & 0x80808080u;  // signs of codes 0 2 4 6 and 1 3 5 7
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t sel = mag >> (16 * h);
+        const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel) | __byte_perm(even, odd, h ? 0x7362 : 0x5140);
+        const uint32_t lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);
+        w[2 * h] = __byte_perm(lo, hi, 0x5140);
+        w[2 * h + 1] = __byte_perm(lo, hi, 0x7362);
+    }
+}
+
+// The values of eight codes, code * s in fp32 (one rounding).
+__device__ __forceinline__ void decode8(uint32_t c, float s, float (&x)[16], int o) {
+    uint32_t w[4];
+    e2m1_bf16x8(c, w);
+    const uint64_t s2 = f2_pack(s, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_unpack(f2_mul(f2_pack(bf16_lo(w[i]), bf16_hi(w[i])), s2), x[o + 2 * i], x[o + 2 * i + 1]);
+}
+
+// The values of sixteen codes to memory, rounded to the type.  bf16: where s is a bf16
+// value (it is whenever the tensor scale is a power of two) the product of two such
+// short significands is exact, and half the instructions.
+__device__ __forceinline__ void store_decoded(__nv_bfloat16 *p, uint32_t lo, uint32_t hi, float s) {
+    uint4 v[2];
+    if ((__float_as_uint(s) & 0xFFFFu) == 0) {
+        const __nv_bfloat162 s2 = __float2bfloat162_rn(s);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            uint32_t w[4];
+            e2m1_bf16x8(q ? hi : lo, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 m = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]), s2);
+                w[i] = *reinterpret_cast<const uint32_t *>(&m);
+            }
+            v[q] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+        float x[16];
+        decode8(lo, s, x, 0);
+        decode8(hi, s, x, 8);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            v[q] = make_uint4(pack_bf16x2(x[8 * q], x[8 * q + 1]), pack_bf16x2(x[8 * q + 2], x[8 * q + 3]),
+                              pack_bf16x2(x[8 * q + 4], x[8 * q + 5]), pack_bf16x2(x[8 * q + 6], x[8 * q + 7]));
+    }
+    reinterpret_cast<uint4 *>(p)[0] = v[0];
+    reinterpret_cast<uint4 *>(p)[1] = v[1];
+}
+__device__ __forceinline__ void store_decoded(float *p, uint32_t lo, uint32_t hi, float s) {
+    float x[16];
+    decode8(lo, s, x, 0);
+    decode8(hi, s, x, 8);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        reinterpret_cast<float4 *>(p)[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
 }
 
 // 16 consecutive values of a row.
@@ -96,78 +181,67 @@ __device__ __forceinline__ void load16<float>(const float *p, float (&x)[16]) {
     }
 }
 
-__device__ __forceinline__ void store16(__nv_bfloat16 *p, const float (&x)[16]) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-        reinterpret_cast<uint4 *>(p)[q] =
-            make_uint4(pack_bf16x2(x[8 * q], x[8 * q + 1]), pack_bf16x2(x[8 * q + 2], x[8 * q + 3]),
-                       pack_bf16x2(x[8 * q + 4], x[8 * q + 5]), pack_bf16x2(x[8 * q + 6], x[8 * q + 7]));
-}
-__device__ __forceinline__ void store16(float *p, const float (&x)[16]) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-        reinterpret_cast<float4 *>(p)[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
-}
-
 // The place of the scale of row r, block j (fp4 scale tiles: 128 rows by 4 blocks).
 __device__ __forceinline__ int64_t scale_at(int64_t r, int64_t j, int64_t tiles_k) {
     return ((r >> 7) * tiles_k + (j >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (j & 3);
 }
 
-// Codes of 16 values and the block's scale byte; `mul` and the returned scale value give
-// the values back: code * scale.
+// Codes of 16 values and the block's scale byte.
 struct Coded {
     uint32_t lo, hi;  // codes 0..7, 8..15
     uint32_t scale;   // byte
     float value;      // what a code of 1 stands for
 };
 
+// max |x|, NaN where a value is NaN.
+__device__ __forceinline__ float abs_max16(const float (&x)[16]) {
+    float m = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = max_nan_abs(m, x[j]);
+    return m;
+}
+
 template <bool NV>
 __device__ __forceinline__ Coded encode(float (&x)[16], float g, float inv_g) {
     Coded c;
+    float amax = abs_max16(x);
     if (NV) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = __fmul_rn(x[j], inv_g);
+        // rounding keeps order, so the largest |RN(x inv_g)| is that of the largest |x|
+        amax = __fmul_rn(amax, inv_g);
+    } else {  // two threads hold a block of 32
+        const float o = __shfl_xor_sync(0xffffffffu, amax, 1);
+        amax = max_nan_abs(amax, o);
     }
-    float amax = 0.0f;
-    bool finite = true;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        amax = fmaxf(amax, fabsf(x[j]));
-        finite = finite && fabsf(x[j]) <= FLT_MAX;
-    }
-    if (!NV) {  // two threads hold a block of 32
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        finite = __shfl_xor_sync(0xffffffffu, finite, 1) && finite;
-    }
-    float s;
+    const bool finite = amax <= FLT_MAX;
     if (NV) {
         c.scale = e4m3(__fdiv_rn(amax, 6.0f));
-        s = e4m3_value(c.scale);
+        const float s = e4m3_value(c.scale);
         c.value = __fmul_rn(s, g);
-        // x / s, correctly rounded: with r = RN(1/s) and q = RN(x r), the residual
-        // x - q s is exact in one fma and RN(q + residual r) is RN(x / s) (Markstein 1990)
+        // x' = RN(x inv_g), then x' / s correctly rounded: with r = RN(1/s) and q = RN(x' r)
+        // the residual x' - q s is exact in one fma, and RN(q + residual r) is RN(x' / s)
+        // (Markstein 1990).  The sign is put back for x' = -0.
         const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
+        const uint64_t g2 = f2_pack(inv_g, inv_g), r2 = f2_pack(r, r), s2 = f2_pack(-s, -s);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float q = __fmul_rn(x[j], r);
-            x[j] = copysignf(__fmaf_rn(__fmaf_rn(-q, s, x[j]), r, q), x[j]);  // -0 stays -0
+        for (int j = 0; j < 8; ++j) {
+            const uint64_t v = f2_mul(f2_pack(x[2 * j], x[2 * j + 1]), g2);
+            const uint64_t q = f2_mul(v, r2);
+            float lo, hi;
+            f2_unpack(f2_fma(f2_fma(q, s2, v), r2, q), lo, hi);
+            x[2 * j] = __uint_as_float(__float_as_uint(lo) | (__float_as_uint(x[2 * j]) & 0x80000000u));
+            x[2 * j + 1] = __uint_as_float(__float_as_uint(hi) | (__float_as_uint(x[2 * j + 1]) & 0x80000000u));
         }
     } else {
         const uint32_t e = __float_as_uint(amax) >> 23;
         c.scale = e > 2u ? e - 2u : 0u;
         c.value = e8m0_value(c.scale);
         const float r = __uint_as_float((254u - c.scale) << 23);  // 2^(127 - byte)
+        const uint64_t r2 = f2_pack(r, r);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = __fmul_rn(x[j], r);
+        for (int j = 0; j < 8; ++j) f2_unpack(f2_mul(f2_pack(x[2 * j], x[2 * j + 1]), r2), x[2 * j], x[2 * j + 1]);
     }
-    c.lo = 0;
-    c.hi = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        c.lo |= e2m1x2(x[2 * j], x[2 * j + 1]) << (8 * j);
-        c.hi |= e2m1x2(x[8 + 2 * j], x[9 + 2 * j]) << (8 * j);
-    }
+    c.lo = e2m1x8(x, 0);
+    c.hi = e2m1x8(x, 8);
     if (!finite) {
         c.scale = NV ? 0x7Fu : 0xFFu;
         c.value = NAN;
@@ -188,22 +262,39 @@ struct PackArgs {
     int64_t tiles_k;  // scale tiles along a row
 };
 
-// One warp per 512-value segment of a row.  CODES: codes and scale tiles (whose padding,
-// rows past N and blocks past K / block, is written as zero); VALUES: the values that the
-// codes stand for, rounded to T.
+// Walks the 512-value segments of rows, one warp each, without a division per segment.
+struct Segments {
+    int64_t row, drow;
+    int seg, dseg, segs;
+    __device__ __forceinline__ Segments(int64_t segs_) : segs(static_cast<int>(segs_)) {
+        const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
+        const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * kThreads) >> 5;
+        row = warp / segs_;
+        seg = static_cast<int>(warp - row * segs_);
+        drow = nwarps / segs_;
+        dseg = static_cast<int>(nwarps - drow * segs_);
+    }
+    __device__ __forceinline__ void next() {
+        row += drow;
+        seg += dseg;
+        if (seg >= segs) {
+            seg -= segs;
+            ++row;
+        }
+    }
+};
+
+// CODES: codes and scale tiles (whose padding, rows past N and blocks past K / block, is
+// written as zero); VALUES: the values that the codes stand for, rounded to T.
 template <typename T, bool NV, bool CODES, bool VALUES>
-__global__ void __launch_bounds__(kThreads) k_encode_fp4(const PackArgs a) {
+__global__ void __launch_bounds__(kThreads, 5) k_encode_fp4(const PackArgs a) {
     pdl_wait();
     pdl_allow_dependents();
     const int lane = threadIdx.x & 31;
     const float g = NV && a.g ? __ldg(a.g) : 1.0f;
     const float inv_g = __fdiv_rn(1.0f, g);
-    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * kThreads) >> 5;
-    const int64_t units = a.rows * a.segs;
-    for (int64_t u = warp; u < units; u += nwarps) {
-        const int64_t row = u / a.segs;
-        const int64_t k0 = (u - row * a.segs) * 512 + lane * 16;
+    for (Segments u(a.segs); u.row < a.rows; u.next()) {
+        const int64_t row = u.row, k0 = static_cast<int64_t>(u.seg) * 512 + lane * 16;
         const bool in = row < a.N && k0 < a.K;
         float x[16];
         if (in) {
@@ -225,14 +316,7 @@ __global__ void __launch_bounds__(kThreads) k_encode_fp4(const PackArgs a) {
             if (lane % (4 * per) == 0 && block / 4 < a.tiles_k)
                 *reinterpret_cast<uint32_t *>(a.scales + scale_at(row, block, a.tiles_k)) = w;
         }
-        if (VALUES && in) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                x[j] = __fmul_rn(e2m1_value((c.lo >> (4 * j)) & 15u), c.value);
-                x[8 + j] = __fmul_rn(e2m1_value((c.hi >> (4 * j)) & 15u), c.value);
-            }
-            store16(static_cast<T *>(a.values) + row * a.K + k0, x);
-        }
+        if (VALUES && in) store_decoded(static_cast<T *>(a.values) + row * a.K + k0, c.lo, c.hi, c.value);
     }
 }
 
@@ -245,22 +329,12 @@ __global__ void __launch_bounds__(kThreads) k_dequant_fp4(const uint8_t *__restr
     pdl_allow_dependents();
     const int lane = threadIdx.x & 31;
     const float g = NV && g_ptr ? __ldg(g_ptr) : 1.0f;
-    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * kThreads) >> 5;
-    for (int64_t u = warp; u < N * segs; u += nwarps) {
-        const int64_t row = u / segs;
-        const int64_t k0 = (u - row * segs) * 512 + lane * 16;
+    for (Segments u(segs); u.row < N; u.next()) {
+        const int64_t k0 = static_cast<int64_t>(u.seg) * 512 + lane * 16;
         if (k0 >= K) continue;
-        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(codes + (row * K + k0) / 2));
-        const uint32_t b = __ldg(scales + scale_at(row, k0 / (NV ? 16 : 32), tiles_k));
-        const float s = NV ? __fmul_rn(e4m3_value(b), g) : e8m0_value(b);
-        float x[16];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = __fmul_rn(e2m1_value((c.x >> (4 * j)) & 15u), s);
-            x[8 + j] = __fmul_rn(e2m1_value((c.y >> (4 * j)) & 15u), s);
-        }
-        store16(out + row * K + k0, x);
+        const uint2 c = __ldg(reinterpret_cast<const uint2 *>(codes + (u.row * K + k0) / 2));
+        const uint32_t b = __ldg(scales + scale_at(u.row, k0 / (NV ? 16 : 32), tiles_k));
+        store_decoded(out + u.row * K + k0, c.x, c.y, NV ? __fmul_rn(e4m3_value(b), g) : e8m0_value(b));
     }
 }
 

@@ -958,24 +958,28 @@ __device__ void prepare_slots(const DistillArgs &a, int64_t t, const RawSlots &r
     }
     RowSums own{-FLT_MAX, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-        if (first[i]) own.m = fmaxf(own.m, x[i]);
+    for (int i = 0; i < PER; ++i) own.m = fmaxf(own.m, first[i] ? x[i] : -FLT_MAX);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, off));
         own.m = fmaxf(own.m, __shfl_xor_sync(0xffffffffu, own.m, off));
     }
     any = __any_sync(0xffffffffu, any);
-    const double shift = TAIL || !any ? 0.0 : static_cast<double>(tm);
-    double e[PER], qsum = 0.0;
+    // The masses.  What they leave of 1 (TAIL) keeps its relative accuracy only if they
+    // are exact beyond fp32; renormalised, expf (within 2 ulp) does.
+    const float shift = TAIL || !any ? 0.0f : tm;
+    float e[PER];
+    double qsum = 0.0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        e[i] = 0.0;
-        if (id[i] >= 0) {
-            e[i] = exp(static_cast<double>(tl[i]) - shift);
-            qsum += e[i];
+        e[i] = 0.0f;
+        if (32 * i < a.k) {  // the same in all lanes
+            const float l = id[i] >= 0 ? tl[i] : -INFINITY;
+            const double d = TAIL ? exp(static_cast<double>(l)) : static_cast<double>(expf(l - shift));
+            e[i] = static_cast<float>(d);
+            qsum += d;
         }
-        if (first[i]) own.S += ex2((x[i] - own.m) * a.c);
+        own.S += first[i] ? ex2((x[i] - own.m) * a.c) : 0.0f;
     }
     qsum = warp_sum(qsum);
 #pragma unroll
@@ -983,7 +987,7 @@ __device__ void prepare_slots(const DistillArgs &a, int64_t t, const RawSlots &r
     bad = bad || !(qsum < INFINITY);
     bad = __any_sync(0xffffffffu, bad);
     twice = __any_sync(0xffffffffu, twice);
-    const double inv = TAIL ? 1.0 : 1.0 / qsum;
+    const float inv = TAIL ? 1.0f : static_cast<float>(1.0 / qsum);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int j = lane + 32 * i;
@@ -991,7 +995,7 @@ __device__ void prepare_slots(const DistillArgs &a, int64_t t, const RawSlots &r
         sl.x[j] = x[i];
         sl.tl[j] = tl[i];
         sl.first[j] = first[i];
-        sl.q[j] = static_cast<float>(e[i] * inv);
+        sl.q[j] = e[i] * inv;
     }
     if (lane == 0) {
         sl.own = own;
@@ -1034,26 +1038,31 @@ __device__ __forceinline__ RowState row_state(const DistillArgs &a, const Slots 
 template <bool TAIL>
 __device__ void finish_slots(const DistillArgs &a, Slots &sl, const RowSums &s, const RowState &r, int64_t t) {
     const int lane = threadIdx.x & 31, k = a.k;
+    // ln S, and q_r ln (q_r / p_r) of the masses outside the slots
     const double lnS = log(static_cast<double>(r.all.S));
-    const double up = static_cast<double>(sl.w) * a.inv_tau, inv_S = 1.0 / static_cast<double>(r.all.S);
+    const double rest = r.live ? sl.qr * (log(sl.qr * r.all.S / s.S) - (static_cast<double>(s.m) - r.all.m) * a.inv_tau)
+                               : 0.0;
+    const float up = sl.w * static_cast<float>(a.inv_tau), inv_S = 1.0f / r.all.S;
     double L = 0.0;
-    for (int i = lane; i < k; i += 32) {
-        if (sl.id[i] < 0) continue;
-        double q = sl.q[i];
-        const double d = static_cast<double>(sl.x[i]) - r.all.m;
-        if (q > 0.0) L += q * (static_cast<double>(sl.tl[i]) - sl.logq0 - (d * a.inv_tau - lnS));
-        if (sl.first[i]) {
+#pragma unroll
+    for (int i = 0; i < kTopMax / 32; ++i) {
+        const int j = lane + 32 * i;
+        float q = sl.q[j];
+        const float x = sl.x[j], y = x - r.all.m;
+        const bool use = sl.id[j] >= 0;
+        if (use && q > 0.0f)
+            L += static_cast<double>(q) * (static_cast<double>(sl.tl[j]) - sl.logq0 -
+                                           ((static_cast<double>(x) - r.all.m) * a.inv_tau - lnS));
+        if (use && sl.first[j]) {
             if (sl.dup) {  // an id given more than once carries its slots' masses together
-                q = 0.0;
-                for (int j = 0; j < k; ++j)
-                    if (sl.id[j] == sl.id[i]) q += sl.q[j];
+                q = 0.0f;
+                for (int m = 0; m < k; ++m)
+                    if (sl.id[m] == sl.id[j]) q += sl.q[m];
             }
-            sl.x[i] = r.nan ? NAN : static_cast<float>(up * (ex2(static_cast<float>(d) * a.c) * inv_S - q));
+            sl.x[j] = r.nan ? NAN : up * (ex2(y * a.c) * inv_S - q);
         }
     }
-    L = warp_sum(L);
-    if (r.live)
-        L += sl.qr * (log(sl.qr) - (log(static_cast<double>(s.S)) + (static_cast<double>(s.m) - r.all.m) * a.inv_tau - lnS));
+    L = warp_sum(L) + rest;
     if (lane == 0 && a.loss) a.loss[t] = r.zero ? 0.0f : r.nan ? NAN : static_cast<float>(sl.w * L);
     __syncwarp();
 }
