@@ -131,6 +131,15 @@ struct Vec<__nv_bfloat16> {
         r.z = i == 2 ? (r.z & keep) | put : r.z;
         r.w = i == 3 ? (r.w & keep) | put : r.w;
     }
+    // elements j with bit j set become -inf
+    static __device__ __forceinline__ void fill(uint4 &r, uint32_t bits) {
+        auto word = [&](uint32_t w, int i) {
+            const uint32_t lo = (bits >> (2 * i)) & 1u ? 0xFF80u : w & 0xFFFFu;
+            const uint32_t hi = (bits >> (2 * i + 1)) & 1u ? 0xFF800000u : w & 0xFFFF0000u;
+            return lo | hi;
+        };
+        r = make_uint4(word(r.x, 0), word(r.y, 1), word(r.z, 2), word(r.w, 3));
+    }
     static __device__ __forceinline__ uint32_t raw(const __nv_bfloat16 *p) {
         return *reinterpret_cast<const unsigned short *>(p);
     }
@@ -183,6 +192,12 @@ struct Vec<float> {
         r.y = j == 1 ? raw : r.y;
         r.z = j == 2 ? raw : r.z;
         r.w = j == 3 ? raw : r.w;
+    }
+    static __device__ __forceinline__ void fill(uint4 &r, uint32_t bits) {
+        r.x = bits & 1u ? kFill : r.x;
+        r.y = bits & 2u ? kFill : r.y;
+        r.z = bits & 4u ? kFill : r.z;
+        r.w = bits & 8u ? kFill : r.w;
     }
     static __device__ __forceinline__ uint32_t raw(const float *p) { return __float_as_uint(*p); }
     static __device__ __forceinline__ float value(const uint4 &r, int j) {
@@ -905,44 +920,61 @@ __device__ __forceinline__ double warp_sum(double v) {
     return v;
 }
 
-// A lane's slots of a row as they come from memory, asked for a row before they are used.
+// A row's slots as they come from memory, each lane its own, two rows before they are
+// used (asynchronous copies, so that no register waits for them).
 struct RawSlots {
-    static constexpr int PER = kTopMax / 32;
-    int64_t id[PER];
-    float tl[PER], w;
-    __device__ __forceinline__ void fetch(const DistillArgs &a, int64_t t) {
-        const int lane = threadIdx.x & 31;
-        w = 0.0f;
-        if (t >= a.T) return;
-        w = a.weight ? a.weight[t] : 1.0f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int j = lane + 32 * i;
-            id[i] = j < a.k ? a.ids[t * a.k + j] : -1;
-            tl[i] = j < a.k ? a.tlp[t * a.k + j] : -INFINITY;
-        }
-    }
+    int64_t id[kTopMax];
+    float tl[kTopMax];
 };
+constexpr int kSlotsPerLane = kTopMax / 32;
+
+__device__ __forceinline__ float fetch_slots(const DistillArgs &a, int64_t t, RawSlots &raw) {
+    const int lane = threadIdx.x & 31;
+    if (t >= a.T) return 0.0f;
+    for (int j = lane; j < a.k; j += 32) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(&raw.id[j])), "l"(a.ids + t * a.k + j)
+                     : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(&raw.tl[j])), "l"(a.tlp + t * a.k + j)
+                     : "memory");
+    }
+    return a.weight ? a.weight[t] : 1.0f;  // 0 for no row: nothing of it is read
+}
+
+// The logits at a row's slots, asked for a row before they are used.
+template <typename T>
+__device__ __forceinline__ void gather_slots(const DistillArgs &a, int64_t t, const RawSlots &raw, float w,
+                                             float (&x)[kSlotsPerLane]) {
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    const T *p = static_cast<const T *>(a.x) + t * a.ld;
+#pragma unroll
+    for (int i = 0; i < kSlotsPerLane; ++i) {
+        const int j = (threadIdx.x & 31) + 32 * i;
+        const int64_t id = j < a.k && w != 0.0f ? raw.id[j] : -1;
+        x[i] = id >= 0 && id < a.V ? Vec<T>::load(p + id) : -INFINITY;
+    }
+}
 
 // One warp: a row's slots, marked in the bitmap, and the teacher's side of the loss.
 template <typename T, bool TAIL>
-__device__ void prepare_slots(const DistillArgs &a, int64_t t, const RawSlots &raw, Slots &sl, uint32_t *bitmap) {
+__device__ void prepare_slots(const DistillArgs &a, int64_t t, const RawSlots &raw, float w,
+                              const float (&x)[kSlotsPerLane], Slots &sl, uint32_t *bitmap) {
     const int lane = threadIdx.x & 31;
-    if (lane == 0) sl.w = raw.w;
-    if (raw.w == 0.0f) return;  // nothing of the row is read
+    if (lane == 0) sl.w = w;
+    if (w == 0.0f) return;  // nothing of the row is read
     const T *p = static_cast<const T *>(a.x) + t * a.ld;
     const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
-    constexpr int PER = RawSlots::PER;
+    constexpr int PER = kSlotsPerLane;
     int id[PER];
-    float x[PER], tl[PER];
+    float tl[PER];
     bool first[PER], bad = false, twice = false, any = false;
     float tm = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        tl[i] = raw.tl[i];
-        bad = bad || raw.id[i] >= a.V;
-        id[i] = raw.id[i] < 0 || raw.id[i] >= a.V ? -1 : static_cast<int>(raw.id[i]);
-        x[i] = id[i] >= 0 ? Vec<T>::load(p + id[i]) : -INFINITY;
+        const int j = lane + 32 * i;
+        const int64_t g = j < a.k ? raw.id[j] : -1;
+        tl[i] = j < a.k ? raw.tl[j] : -INFINITY;
+        bad = bad || g >= a.V;
+        id[i] = g < 0 || g >= a.V ? -1 : static_cast<int>(g);
     }
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -1087,6 +1119,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const Dis
     constexpr int P = kThreads + 32;  // walkers and slot warp
     __shared__ RowSums buf[2][P / 32];
     __shared__ Slots slots[2];
+    __shared__ RawSlots raw[2];  // of odd and even rows
     __shared__ RingCtl ctl;
     const int tid = threadIdx.x;
     const bool walker = tid < kThreads;
@@ -1112,11 +1145,16 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const Dis
         return;
     }
     int turn = 0;
-    RawSlots raw;
+    // the slot warp: logits at the next row's slots, its weight, and that of the row after it
+    float xs[kSlotsPerLane], w_next = 0.0f, w_ahead = 0.0f;
+    const int64_t step = gridDim.x;
     if (!walker) {
-        raw.fetch(a, blockIdx.x);
-        prepare_slots<T, TAIL>(a, blockIdx.x, raw, slots[0], bitmaps);
-        raw.fetch(a, static_cast<int64_t>(blockIdx.x) + gridDim.x);
+        const float w0 = fetch_slots(a, blockIdx.x, raw[0]);
+        gather_slots<T>(a, blockIdx.x, raw[0], w0, xs);
+        w_next = fetch_slots(a, blockIdx.x + step, raw[1]);
+        prepare_slots<T, TAIL>(a, blockIdx.x, raw[0], w0, xs, slots[0], bitmaps);
+        gather_slots<T>(a, blockIdx.x + step, raw[1], w_next, xs);
+        w_ahead = fetch_slots(a, blockIdx.x + 2 * step, raw[0]);
     }
     bar<P>();
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
@@ -1132,11 +1170,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const Dis
             auto mask = [&](uint4 &r, int v) {
                 const int at = v * Vec<T>::N;
                 const uint32_t bits = (bitmap[at >> 5] >> (at & 31)) & ((1u << Vec<T>::N) - 1u);
-                if (bits) {
-#pragma unroll 1
-                    for (int j = 0; j < Vec<T>::N; ++j)
-                        if ((bits >> j) & 1u) Vec<T>::set(r, j, Vec<T>::kFill);
-                }
+                if (bits) Vec<T>::fill(r, bits);
             };
             ring_walk(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int n) {
                 if (TAIL) {
@@ -1154,9 +1188,11 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const Dis
             }
             const RowSums mine_w = warp_join(mine, a.c);
             if ((tid & 31) == 0) buf[turn][tid >> 5] = mine_w;
-        } else if (!walker && t + gridDim.x < a.T) {
-            prepare_slots<T, TAIL>(a, t + gridDim.x, raw, slots[turn ^ 1], bitmaps + (turn ^ 1) * words);
-            raw.fetch(a, t + 2 * static_cast<int64_t>(gridDim.x));
+        } else if (!walker && t + step < a.T) {
+            prepare_slots<T, TAIL>(a, t + step, raw[turn ^ 1], w_next, xs, slots[turn ^ 1], bitmaps + (turn ^ 1) * words);
+            gather_slots<T>(a, t + 2 * step, raw[turn], w_ahead, xs);
+            w_next = w_ahead;
+            w_ahead = fetch_slots(a, t + 3 * step, raw[turn ^ 1]);
         }
         bar<P>();
         RowSums s;
