@@ -336,21 +336,28 @@ __device__ __forceinline__ int chunks_of(const Row<T> &row) {
     return (row.b1 - row.b0 + kChunk - 1) / kChunk;
 }
 
-// One thread: the row's chunks, once.  A wait that runs out raises the block's abort
+// One thread: the row's chunks, once; `again`: they will be read a second time, so L2 is
+// to keep them, and otherwise to let them go first.  A wait that runs out raises the block's abort
 // flag, after which every wait returns at once: the block runs to its end on what the
 // ring holds, and the device error word tells.
 template <typename T>
-__device__ __forceinline__ void ring_fill(const Row<T> &row, uint4 *ring, RingCtl &ctl, RingPos &pos, int *err) {
+__device__ __forceinline__ void ring_fill(const Row<T> &row, uint4 *ring, RingCtl &ctl, RingPos &pos, int *err,
+                                          bool again) {
     const int chunks = chunks_of(row);
+    uint64_t policy;
+    if (again)
+        asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
+    else
+        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     for (int c = 0; c < chunks; ++c, pos.next()) {
         if (!mbar_wait_bounded(&ctl.empty[pos.stage], pos.phase ^ 1u, &ctl.abort_flag, err, kWaitLimitNs)) return;
         const int v = row.b0 + c * kChunk;
         const uint32_t bytes = static_cast<uint32_t>(min(kChunk, row.b1 - v)) * 16u;
         mbar_arrive_expect_tx(&ctl.full[pos.stage], bytes);
         asm volatile(
-            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+            "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
                 smem_u32(ring + pos.stage * kChunk)),
-            "l"(row.vec(v)), "r"(bytes), "r"(smem_u32(&ctl.full[pos.stage]))
+            "l"(row.vec(v)), "r"(bytes), "r"(smem_u32(&ctl.full[pos.stage])), "l"(policy)
             : "memory");
     }
 }
@@ -815,7 +822,7 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) k_token_logprobs(co
     };
     if (threadIdx.x >= kThreads) {
         if (threadIdx.x == kThreads) {
-            for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) ring_fill(row_of(t), ring, ctl, pos, a.err);
+            for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) ring_fill(row_of(t), ring, ctl, pos, a.err, false);
             ring_end(ctl);
         }
         return;
@@ -1137,8 +1144,8 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const Dis
         if (tid == P) {
             for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
                 if (a.weight && a.weight[t] == 0.0f) continue;
-                ring_fill(row_of(a.x, t), ring, ctl, pos, a.err);
-                if (a.dx) ring_fill(row_of(a.x, t), ring, ctl, pos, a.err);
+                ring_fill(row_of(a.x, t), ring, ctl, pos, a.err, a.dx != nullptr);
+                if (a.dx) ring_fill(row_of(a.x, t), ring, ctl, pos, a.err, false);
             }
             ring_end(ctl);
         }
