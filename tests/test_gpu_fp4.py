@@ -134,7 +134,10 @@ def values(t, fmt, g):
 
 CASES = [(1, 8, 32), (1, 128, 256), (2, 136, 64), (7, 264, 320), (16, 512, 1024), (17, 128, 96), (33, 392, 4096),
          (64, 72, 2048), (65, 1000, 512), (128, 256, 288), (129, 264, 320), (300, 520, 1184), (257, 8, 4096),
-         (515, 768, 2048)]
+         (515, 768, 2048),
+         # few tokens: K split over the ranks of a cluster, ranks with uneven and with no parts, K past what is
+         # packed in the product
+         (1, 136, 8192), (16, 264, 4096), (3, 72, 2336), (5, 64, 32768), (13, 1032, 1312), (2, 40, 33024)]
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
@@ -212,6 +215,7 @@ def test_workspaces_outputs_and_empty_calls():
     g = scale_of(W, fmt)
     codes, scales = packed(W, fmt, g)
     want = eqat.fp4_linear_fwd(X, codes, scales, fmt, tscale=g)
+    assert eqat.fp4_workspace(16, N, K, fmt).numel() == 1  # nothing needed
     ws = eqat.fp4_workspace(M, N, K, fmt).fill_(255)
     Y = torch.full((M, N), float("nan"), dtype=torch.bfloat16, device="cuda")
     got = eqat.fp4_linear_fwd(X, codes, scales, fmt, tscale=g, ws=ws, Y=Y)

@@ -164,7 +164,7 @@ def test_fp4_refusals(lib):
     assert lib.eqat_dequant_fp4(P(FAKE), P(FAKE), 3, 64, 1, P(FAKE), P(FAKE), 2, st) == DTYPE
     assert lib.eqat_fp4_tensor_scale(P(FAKE), 1, 33, P(FAKE), st) == SHAPE
     assert lib.eqat_fp4_tensor_scale(P(FAKE), 1, 32, P(0), st) == NULL
-    fwd = lambda X=FAKE, N=16, K=64, fmt=0, g=0, ws=FAKE, n=1 << 20, M=3: lib.eqat_fp4_linear_fwd(  # noqa: E731
+    fwd = lambda X=FAKE, N=16, K=64, fmt=0, g=0, ws=FAKE, n=1 << 20, M=17: lib.eqat_fp4_linear_fwd(  # noqa: E731
         P(X), P(FAKE), P(FAKE), fmt, P(g), P(g), P(FAKE), M, N, K, P(ws), n, st)
     assert fwd(N=12) == SHAPE and fwd(K=40) == SHAPE and fwd(fmt=3) == UNSUP and fwd(g=FAKE) == UNSUP
     assert fwd(ws=0) == WS and fwd(n=100) == WS and fwd(ws=FAKE + 16) == ALIGN
@@ -174,7 +174,8 @@ def test_fp4_refusals(lib):
     assert bwd(dY=0) == NULL and bwd(dX=FAKE + 2) == ALIGN and bwd(n=8) == WS and bwd(dX=0, dW=0) == OK
     assert lib.eqat_fp4_scale_bytes(129, 96, 1) == 2 * 2 * 512  # 6 blocks of 16: two tiles along K
     assert lib.eqat_fp4_scale_bytes(128, 96, 0) == 512 and lib.eqat_fp4_scale_bytes(1, 20, 0) == 0
-    assert lib.eqat_fp4_workspace_bytes(3, 16, 64, 0, 0) == 256 + 512
+    assert lib.eqat_fp4_workspace_bytes(3, 16, 64, 0, 0) == 0  # packed inside the product
+    assert lib.eqat_fp4_workspace_bytes(17, 16, 64, 0, 0) == 768 + 512
     assert lib.eqat_fp4_workspace_bytes(3, 16, 64, 0, 1) == 16 * 64 * 2 + 512
 
 

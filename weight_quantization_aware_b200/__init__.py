@@ -559,7 +559,7 @@ def token_logprobs(logits, targets, top_k=0, temperature=1.0):
     T, V, ld = _rows(logits, "logits", dev)
     tp = _arg(targets, "targets", torch.int64, (T,), dev)
     where = logits.device
-    lp, ent = (torch.empty(T, dtype=torch.float32, device=where) for _ in range(2))
+    lp, ent = torch.empty_like(targets, dtype=torch.float32), torch.empty_like(targets, dtype=torch.float32)
     ids = top = None
     if top_k > 0:
         ids = torch.empty((T, top_k), dtype=torch.int64, device=where)
@@ -732,8 +732,11 @@ def _fp4_operands(X, codes, scales, fmt, tscale, x_tscale, dev):
 
 def _fp4_ws(ws, M, N, K, fmt, backward, dev, like):
     if ws is None:
-        ws = fp4_workspace(M, N, K, fmt, backward, like.device)
-        return ws, ws.data_ptr(), ws.numel()
+        n = _lib.eqat_fp4_workspace_bytes(M, N, K, _FP4_FMT[fmt], backward)
+        if n == 0:
+            return None, None, 0
+        ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+        return ws, ws.data_ptr(), n
     return ws, _arg(ws, "ws", torch.uint8, ws.shape, dev), ws.numel()
 
 

@@ -19,6 +19,7 @@
 #include <atomic>
 #include <cstdint>
 
+#include "eqat_fp4.cuh"
 #include "eqat_internal.h"
 #include "eqat_pdl.cuh"
 #include "eqat_ptx.cuh"
@@ -603,6 +604,232 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
     }
 }
 
+// ---------------------------------------------------------------------------- few tokens
+// Up to 16 tokens in one launch: the weights are the rows of a tile of 128 x 16, a cluster
+// of CTAs splits K, and each CTA packs its part of X into the swizzled operand tiles and
+// scale tiles itself while the first weights are on their way.  The parts are joined over
+// the cluster's shared memory in the order of the ranks.  The call reads the packed
+// weights once; it is bound by launch and memory latency (the weights of a 4096 x 4096
+// layer are 1.4 us of HBM time).
+constexpr int kDecTokens = 16;
+constexpr int kDecThreads = 256;    // producer, issuer (after packing), packers, of which four drain
+constexpr int kDecMaxSlice = 4096;  // K values of a CTA
+constexpr int kDecStages = 6;
+
+template <bool NV>
+struct DecCfg {
+    static constexpr int SF = NV ? 4 : 2;
+    static constexpr int KSF = NV ? 64 : 128;
+    static constexpr int STAGE = kATile + 2048;  // A and its scale tiles (mx uses half of that)
+    static constexpr int XTILE = kDecTokens * 128;
+    static constexpr int XSTAGES = kDecMaxSlice / kKStage;
+    static constexpr int RED = 128 * (kDecTokens + 1) * 4;
+    static constexpr int SMEM = 1024 + kDecStages * STAGE + XSTAGES * (XTILE + SF * kSfTile) + RED + 256;
+    static constexpr int SF_COLS = SF * 8;
+    static_assert(32 + kDecStages * SF_COLS <= 512 && SMEM <= 232448, "tensor and shared memory");
+};
+
+struct DecArgs {
+    const __nv_bfloat16 *X;
+    const uint8_t *sf;
+    const float *gx, *gw;
+    __nv_bfloat16 *Y;
+    int64_t sf_tiles_k, N, K;
+    int M, slice;  // K values per rank, a multiple of kKStage
+    int *err;
+    uint64_t wait_limit_ns;
+};
+
+struct DecCtl {
+    uint64_t full[kDecStages], empty[kDecStages], acc_full, drain;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+static_assert(sizeof(DecCtl) <= 256, "control block exceeds its slot");
+
+// Packs the CTA's slice of X: token r, values k0 .. k0 + 15 of the slice per step.
+template <bool NV>
+__device__ __forceinline__ void pack_slice(const DecArgs &p, int64_t kbase, int klen, uint8_t *xt, uint8_t *xs, int first,
+                                           int count) {
+    using C = DecCfg<NV>;
+    const float g = NV && p.gx ? __ldg(p.gx) : 1.0f, inv_g = __fdiv_rn(1.0f, g);
+    const int per_row = (klen + 63) / 64 * 4;  // the last MMA's values past K are packed as 0
+    const int total = p.M * per_row;
+    for (int i0 = first - (first & 31); i0 < total; i0 += count) {
+        const int i = i0 + (first & 31);
+        const int r = i / per_row, k = (i - r * per_row) * 16;
+        const bool live = i < total, in = live && k < klen;
+        float x[16];
+        if (in) {
+            fp4::load16<__nv_bfloat16>(p.X + static_cast<int64_t>(r) * p.K + kbase + k, x);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = 0.0f;
+        }
+        const fp4::Coded c = fp4::encode<NV>(x, g, inv_g);
+        if (!live) continue;
+        const int st = k / kKStage, byte = (k % kKStage) / 2;
+        *reinterpret_cast<uint2 *>(xt + st * C::XTILE + r * 128 + (((byte >> 4) ^ (r & 7)) << 4) + (byte & 8)) =
+            make_uint2(c.lo, c.hi);
+        const int block = k / (NV ? 16 : 32);
+        if (NV || (k & 16) == 0) xs[(block / 4) * kSfTile + r * 16 + (block & 3)] = in ? c.scale : 0;
+    }
+}
+
+template <bool NV>
+__global__ void __launch_bounds__(kDecThreads, 1) k_decode_fp4(const __grid_constant__ CUtensorMap tmW, const DecArgs p) {
+    using C = DecCfg<NV>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    uint8_t *xt = smem + kDecStages * C::STAGE, *xs = xt + C::XSTAGES * C::XTILE;
+    float *red = reinterpret_cast<float *>(xs + C::XSTAGES * C::SF * kSfTile);
+    DecCtl *ctl = reinterpret_cast<DecCtl *>(reinterpret_cast<uint8_t *>(red) + C::RED);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank, nranks;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nranks));
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kDecStages; ++i) {
+            mbar_init(&ctl->full[i], 1);
+            mbar_init(&ctl->empty[i], 1);
+        }
+        mbar_init(&ctl->acc_full, 1);
+        mbar_init(&ctl->drain, 1);
+        ctl->abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tmW);
+    }
+    pdl_wait();
+    if (threadIdx.x == 0) pdl_allow_dependents();
+    if (warp == 2) {
+        tmem_alloc(&ctl->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    volatile int *abort_flag = &ctl->abort_flag;
+    const int tile = blockIdx.x / nranks;
+    const int64_t kbase = static_cast<int64_t>(rank) * p.slice;
+    const int klen = static_cast<int>(p.K - kbase < p.slice ? (p.K > kbase ? p.K - kbase : 0) : p.slice);
+    const int nkb = (klen + kKStage - 1) / kKStage;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (elect_one_sync()) {
+            uint32_t armed = 0, armed_parity = 0;
+            for (int kb = 0; kb < nkb; ++kb) {
+                const int st = kb % kDecStages;
+                const uint32_t ph = (kb / kDecStages) & 1u;
+                if (!mbar_wait_bounded(&ctl->empty[st], ph ^ 1u, abort_flag, p.err, p.wait_limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *sa = smem + st * C::STAGE;
+                const int64_t sf0 = kbase / C::KSF + static_cast<int64_t>(kb) * C::SF;
+                const int64_t left = p.sf_tiles_k - sf0;
+                const uint32_t sf_bytes = static_cast<uint32_t>(left < C::SF ? left : C::SF) * kSfTile;
+                mbar_arrive_expect_tx(&ctl->full[st], kATile + sf_bytes);
+                armed |= 1u << st;
+                armed_parity = (armed_parity & ~(1u << st)) | (ph << st);
+                tma_load_2d(sa, &tmW, &ctl->full[st], static_cast<int>(kbase / 2) + kb * 128, tile * 128);
+                bulk_load(sa + kATile, p.sf + (tile * p.sf_tiles_k + sf0) * kSfTile, sf_bytes, &ctl->full[st]);
+            }
+            if (!ok) {  // let the copies already issued land before the block exits
+                for (int st = 0; st < kDecStages; ++st)
+                    if (armed & (1u << st)) {
+                        const uint32_t a = smem_u32(&ctl->full[st]);
+                        const uint64_t t0 = globaltimer_ns();
+                        while (!mbar_try_wait(a, (armed_parity >> st) & 1u) && globaltimer_ns() - t0 < 100000000ull) {
+                        }
+                    }
+            }
+        }
+        __syncwarp();
+    } else {
+        pack_slice<NV>(p, kbase, klen, xt, xs, static_cast<int>(threadIdx.x) - 32, kDecThreads - 32);
+        fence_proxy_async_smem();
+        asm volatile("bar.sync 1, %0;" ::"n"(kDecThreads - 32) : "memory");
+    }
+    if (warp == 1) {
+        if (elect_one_sync()) {
+            for (int kb = 0; kb < nkb; ++kb) {
+                const int st = kb % kDecStages;
+                const uint32_t ph = (kb / kDecStages) & 1u;
+                if (!mbar_wait_bounded(&ctl->full[st], ph, abort_flag, p.err, p.wait_limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sa = smem_u32(smem + st * C::STAGE), ssfa = sa + kATile;
+                const uint32_t sb = smem_u32(xt + kb * C::XTILE), ssfb = smem_u32(xs + kb * C::SF * kSfTile);
+                const uint32_t tsf = tmem + 32 + st * C::SF_COLS;
+                const int kleft = klen - kb * kKStage;
+                const int nsf = kleft >= kKStage ? C::SF : (kleft + C::KSF - 1) / C::KSF;
+                for (int j = 0; j < nsf; ++j) {
+                    tmem_cp_scales(tsf + j * 4, smem_desc_plain(ssfa + j * kSfTile));
+                    tmem_cp_scales(tsf + C::SF * 4 + j * 4, smem_desc_plain(ssfb + j * kSfTile));
+                }
+                const int nmma = kleft >= kKStage ? kKStage / 64 : (kleft + 63) / 64;
+                for (int kk = 0; kk < nmma; ++kk) {
+                    const int j = NV ? kk : kk >> 1;
+                    mma_fp4<NV>(tmem, smem_desc_sw128(sa + kk * 32, 16, 1024), smem_desc_sw128(sb + kk * 32, 16, 1024),
+                                idesc_fp4(kDecTokens, NV, NV ? 0u : (kk & 1) * 2u), tsf + j * 4, tsf + C::SF * 4 + j * 4,
+                                (kb > 0 || kk > 0) ? 1u : 0u);
+                }
+                tc_commit(&ctl->empty[st]);
+            }
+            if (ok) {
+                tc_commit(&ctl->acc_full);
+            } else {  // wait for the MMAs already issued before tensor memory is freed
+                tc_commit(&ctl->drain);
+                const uint32_t a = smem_u32(&ctl->drain);
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(a, 0) && globaltimer_ns() - t0 < 100000000ull) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const bool done = mbar_wait_bounded(&ctl->acc_full, 0, abort_flag, p.err, p.wait_limit_ns);
+        if (__all_sync(0xffffffffu, done)) {
+            tc_fence_after();
+            const int row = (warp & 3) * 32 + lane;
+            float v[16];
+            tmem_ld_16cols(tmem + (((warp & 3) * 32) << 16), v);
+            // a rank without a part of K has made no MMA: its part is 0
+#pragma unroll
+            for (int j = 0; j < kDecTokens; ++j) red[row * (kDecTokens + 1) + j] = nkb > 0 ? v[j] : 0.0f;
+        }
+    }
+    tc_fence_before();
+    // the parts are complete in every CTA of the cluster
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    const float alpha = (p.gx ? __ldg(p.gx) : 1.0f) * (p.gw ? __ldg(p.gw) : 1.0f);
+    const int rows = 128 / static_cast<int>(nranks);  // of this rank
+    for (int i = threadIdx.x; i < rows * p.M; i += kDecThreads) {
+        const int row = static_cast<int>(rank) * rows + i % rows, m = i / rows;
+        const int64_t n = static_cast<int64_t>(tile) * 128 + row;
+        float sum = 0.0f;
+        for (uint32_t q = 0; q < nranks; ++q) {
+            float part;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                         : "=f"(part)
+                         : "r"(map_to_rank(&red[row * (kDecTokens + 1) + m], q)));
+            sum = __fadd_rn(sum, part);
+        }
+        if (n < p.N) p.Y[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(__fmul_rn(sum, alpha));
+    }
+    // no CTA leaves while another may read its part
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 struct Side {
     const uint8_t *codes, *scales;
     const float *g;
@@ -705,7 +932,61 @@ cudaError_t dispatch(const Side &x, const Side &w, int64_t K, void *Y, const Dev
     return launch_pair<NV>(x, w, K, Y, dev, st);
 }
 
+template <bool NV>
+cudaError_t launch_decode(const void *X, const float *gx, const Side &w, int64_t M, int64_t K, void *Y,
+                          const DeviceInfo &dev, cudaStream_t st) {
+    using C = DecCfg<NV>;
+    CUtensorMap map;
+    cudaError_t e = encode_map_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, K / 2, w.rows, K / 2, 128, 128,
+                                  CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    auto kern = k_decode_fp4<NV>;
+    static std::atomic<uint64_t> done{0};
+    const uint64_t bit = 1ull << (dev.device & 63);
+    if (!(done.load() & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit);
+    }
+    const int64_t tiles = (w.rows + 127) / 128, stages = (K + kKStage - 1) / kKStage;
+    // ranks: enough for the slice that a CTA can pack, then doubled while the SMs last and
+    // every rank keeps two stages
+    int ranks = 1;
+    while (static_cast<int64_t>(ranks) * kDecMaxSlice < K) ranks *= 2;
+    while (ranks < 8 && 2 * ranks * tiles <= dev.sm_count && stages >= 4 * ranks) ranks *= 2;
+    if (ranks > 8 || tiles * ranks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    DecArgs p{};
+    p.X = static_cast<const __nv_bfloat16 *>(X);
+    p.sf = w.scales;
+    p.gx = gx;
+    p.gw = w.g;
+    p.Y = static_cast<__nv_bfloat16 *>(Y);
+    p.sf_tiles_k = (K / (NV ? 16 : 32) + 3) / 4;
+    p.N = w.rows;
+    p.K = K;
+    p.M = static_cast<int>(M);
+    p.slice = static_cast<int>((stages + ranks - 1) / ranks * kKStage);
+    p.err = device_error_word();
+    if (!p.err) return cudaErrorInvalidSymbol;
+    p.wait_limit_ns = kWaitLimitNs;
+    cudaLaunchAttribute cluster{};
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim.x = static_cast<unsigned>(ranks);
+    cluster.val.clusterDim.y = 1;
+    cluster.val.clusterDim.z = 1;
+    return launch_pdl_ex(kern, dim3(static_cast<unsigned>(tiles * ranks)), dim3(kDecThreads), C::SMEM, st, cluster, map, p);
+}
+
 }  // namespace
+
+bool fp4_packs_in_product(int64_t M, int64_t K) { return M <= kDecTokens && K <= 8ll * kDecMaxSlice; }
+
+cudaError_t launch_fp4_few_tokens(const void *X, const float *gx, const uint8_t *w_codes, const uint8_t *w_scales,
+                                  const float *gw, bool nv, int64_t M, int64_t N, int64_t K, void *Y,
+                                  const DeviceInfo &dev, cudaStream_t st) {
+    const Side w{w_codes, w_scales, gw, N};
+    return nv ? launch_decode<true>(X, gx, w, M, K, Y, dev, st) : launch_decode<false>(X, gx, w, M, K, Y, dev, st);
+}
 
 cudaError_t launch_gemm_fp4(const uint8_t *x_codes, const uint8_t *x_scales, const float *gx, const uint8_t *w_codes,
                             const uint8_t *w_scales, const float *gw, bool nv, int64_t M, int64_t N, int64_t K,
