@@ -388,8 +388,6 @@ __device__ __forceinline__ void ring_walk(const Row<T> &row, const uint4 *ring, 
         if (row.b0 + (c + 1) * kChunk <= row.b1) {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) r[u] = src[u * kThreads];
-            __syncwarp();
-            if ((tid & 31) == 0) mbar_arrive(&ctl.empty[pos.stage]);
             f(r, v, std::integral_constant<int, kUnroll>());
         } else {
             int n = 0;
@@ -399,10 +397,15 @@ __device__ __forceinline__ void ring_walk(const Row<T> &row, const uint4 *ring, 
                 n += in;
                 r[u] = in ? src[u * kThreads] : make_uint4(Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill);
             }
-            __syncwarp();
-            if ((tid & 31) == 0) mbar_arrive(&ctl.empty[pos.stage]);
             f(r, v, n);
         }
+        // The slot is given back when its reads have been performed: arriving right after
+        // the load instructions let the next copy overtake them (a few rows in a
+        // thousand had entries of a later chunk in their sums).  The fence orders these
+        // generic reads before the copy's writes.
+        fence_proxy_async_smem();
+        __syncwarp();
+        if ((tid & 31) == 0) mbar_arrive(&ctl.empty[pos.stage]);
     }
 }
 
