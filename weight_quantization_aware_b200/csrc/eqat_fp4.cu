@@ -56,8 +56,9 @@ struct Segments {
 };
 
 // CODES: codes and scale tiles (whose padding, rows past N and blocks past K / block, is
-// written as zero); VALUES: the values that the codes stand for, rounded to T.
-template <typename T, bool NV, bool CODES, bool VALUES>
+// written as zero); otherwise the values that the codes stand for, rounded to T (V8: they
+// are 32-byte aligned).
+template <typename T, bool NV, bool CODES, bool V8>
 __global__ void __launch_bounds__(kThreads, 5) k_encode_fp4(const PackArgs a) {
     pdl_wait();
     pdl_allow_dependents();
@@ -87,11 +88,11 @@ __global__ void __launch_bounds__(kThreads, 5) k_encode_fp4(const PackArgs a) {
             if (lane % (4 * per) == 0 && block / 4 < a.tiles_k)
                 *reinterpret_cast<uint32_t *>(a.scales + scale_at(row, block, a.tiles_k)) = w;
         }
-        if (VALUES && in) store_decoded(static_cast<T *>(a.values) + row * a.K + k0, c.lo, c.hi, c.value);
+        if (!CODES && in) store_decoded<V8>(static_cast<T *>(a.values) + row * a.K + k0, c.lo, c.hi, c.value);
     }
 }
 
-template <typename T, bool NV>
+template <typename T, bool NV, bool V8>
 __global__ void __launch_bounds__(kThreads) k_dequant_fp4(const uint8_t *__restrict__ codes,
                                                           const uint8_t *__restrict__ scales, const float *g_ptr,
                                                           T *__restrict__ out, int64_t N, int64_t K, int64_t segs,
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) k_dequant_fp4(const uint8_t *__restr
         if (k0 >= K) continue;
         const uint2 c = __ldg(reinterpret_cast<const uint2 *>(codes + (u.row * K + k0) / 2));
         const uint32_t b = __ldg(scales + scale_at(u.row, k0 / (NV ? 16 : 32), tiles_k));
-        store_decoded(out + u.row * K + k0, c.x, c.y, NV ? __fmul_rn(e4m3_value(b), g) : e8m0_value(b));
+        store_decoded<V8>(out + u.row * K + k0, c.x, c.y, NV ? __fmul_rn(e4m3_value(b), g) : e8m0_value(b));
     }
 }
 
@@ -143,6 +144,8 @@ __global__ void __launch_bounds__(kThreads) k_tensor_scale_fp4(const T *__restri
     }
 }
 
+inline bool aligned32(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int grid_of(int64_t warps, const DeviceInfo &dev) {
@@ -153,9 +156,9 @@ int grid_of(int64_t warps, const DeviceInfo &dev) {
 template <typename T, bool NV>
 cudaError_t encode_t(const PackArgs &a, const DeviceInfo &dev, cudaStream_t st) {
     const dim3 grid(grid_of(a.rows * a.segs, dev)), block(kThreads);
-    if (a.codes && a.values) return launch_pdl(k_encode_fp4<T, NV, true, true>, grid, block, 0, st, a);
     if (a.codes) return launch_pdl(k_encode_fp4<T, NV, true, false>, grid, block, 0, st, a);
-    return launch_pdl(k_encode_fp4<T, NV, false, true>, grid, block, 0, st, a);
+    return aligned32(a.values) ? launch_pdl(k_encode_fp4<T, NV, false, true>, grid, block, 0, st, a)
+                               : launch_pdl(k_encode_fp4<T, NV, false, false>, grid, block, 0, st, a);
 }
 
 }  // namespace
@@ -181,15 +184,16 @@ cudaError_t launch_dequant_fp4(const uint8_t *codes, const uint8_t *scales, bool
                                int64_t K, void *out, bool f32, const DeviceInfo &dev, cudaStream_t st) {
     const int64_t segs = cdiv(K, 512), tiles_k = cdiv(K / (nv ? 16 : 32), 4);
     const dim3 grid(grid_of(N * segs, dev)), block(kThreads);
+    auto go = [&](auto kern, auto *o) { return launch_pdl(kern, grid, block, 0, st, codes, scales, g, o, N, K, segs, tiles_k); };
+    const bool v8 = aligned32(out);
     if (f32) {
         float *o = static_cast<float *>(out);
-        return nv ? launch_pdl(k_dequant_fp4<float, true>, grid, block, 0, st, codes, scales, g, o, N, K, segs, tiles_k)
-                  : launch_pdl(k_dequant_fp4<float, false>, grid, block, 0, st, codes, scales, g, o, N, K, segs, tiles_k);
+        if (nv) return v8 ? go(k_dequant_fp4<float, true, true>, o) : go(k_dequant_fp4<float, true, false>, o);
+        return v8 ? go(k_dequant_fp4<float, false, true>, o) : go(k_dequant_fp4<float, false, false>, o);
     }
     __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(out);
-    return nv ? launch_pdl(k_dequant_fp4<__nv_bfloat16, true>, grid, block, 0, st, codes, scales, g, o, N, K, segs, tiles_k)
-              : launch_pdl(k_dequant_fp4<__nv_bfloat16, false>, grid, block, 0, st, codes, scales, g, o, N, K, segs,
-                           tiles_k);
+    if (nv) return v8 ? go(k_dequant_fp4<__nv_bfloat16, true, true>, o) : go(k_dequant_fp4<__nv_bfloat16, true, false>, o);
+    return v8 ? go(k_dequant_fp4<__nv_bfloat16, false, true>, o) : go(k_dequant_fp4<__nv_bfloat16, false, false>, o);
 }
 
 cudaError_t launch_tensor_scale_fp4(const void *x, bool f32, int64_t n, float *out, const DeviceInfo &dev,

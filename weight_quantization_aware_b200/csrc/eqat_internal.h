@@ -192,8 +192,8 @@ cudaError_t launch_distill_topk(const void *x, bool f32, int64_t ld, int64_t T, 
                                 float *loss, void *dx, const DeviceInfo &dev, cudaStream_t st);
 
 // ------------------------------------------------------------------ microscaled 4-bit floats
-// x [N, K] -> codes [N, K / 2], scale tiles, values [N, K] (each nullable; codes and
-// scales together); g: tensor scale of the nv format (nullable: 1).
+// x [N, K] -> codes [N, K / 2] and scale tiles, or (codes and scales NULL) values [N, K];
+// g: tensor scale of the nv format (nullable: 1).
 cudaError_t launch_encode_fp4(const void *x, bool f32, bool nv, const float *g, int64_t N, int64_t K, uint8_t *codes,
                               uint8_t *scales, void *values, const DeviceInfo &dev, cudaStream_t st);
 cudaError_t launch_dequant_fp4(const uint8_t *codes, const uint8_t *scales, bool nv, const float *g, int64_t N,
