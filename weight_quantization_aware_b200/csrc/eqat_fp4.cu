@@ -59,22 +59,28 @@ struct Segments {
 // written as zero); otherwise the values that the codes stand for, rounded to T (V8: they
 // are 32-byte aligned).
 template <typename T, bool NV, bool CODES, bool V8>
-__global__ void __launch_bounds__(kThreads, 5) k_encode_fp4(const PackArgs a) {
+__global__ void __launch_bounds__(kThreads, NV ? 3 : 4) k_encode_fp4(const PackArgs a) {
     pdl_wait();
     pdl_allow_dependents();
     const int lane = threadIdx.x & 31;
     const float g = NV && a.g ? __ldg(a.g) : 1.0f;
     const float inv_g = __fdiv_rn(1.0f, g);
-    for (Segments u(a.segs); u.row < a.rows; u.next()) {
+    // the next segment is on its way while one is encoded
+    auto fetch = [&](const Segments &u) {
+        Raw16<T> r = zero16<T>();
+        const int64_t k0 = static_cast<int64_t>(u.seg) * 512 + lane * 16;
+        if (u.row < a.N && k0 < a.K) r = load_raw16(static_cast<const T *>(a.x) + u.row * a.K + k0);
+        return r;
+    };
+    Segments u(a.segs);
+    Raw16<T> ahead = fetch(u);
+    while (u.row < a.rows) {
         const int64_t row = u.row, k0 = static_cast<int64_t>(u.seg) * 512 + lane * 16;
         const bool in = row < a.N && k0 < a.K;
         float x[16];
-        if (in) {
-            load16<T>(static_cast<const T *>(a.x) + row * a.K + k0, x);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = 0.0f;
-        }
+        unpack16(ahead, x);
+        u.next();
+        ahead = fetch(u);
         Coded c = encode<NV>(x, g, inv_g);
         if (!in) c.scale = 0;
         if (CODES) {

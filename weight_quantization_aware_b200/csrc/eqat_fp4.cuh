@@ -151,31 +151,40 @@ __device__ __forceinline__ void store_decoded(float *p, uint32_t lo, uint32_t hi
     store16<float, V8>(p, x);
 }
 
-// 16 consecutive values of a row.
+// 16 consecutive values of a row, as stored and widened.
 template <typename T>
-__device__ __forceinline__ void load16(const T *p, float (&x)[16]);
+struct Raw16 {
+    Raw8<T> a, b;
+};
+template <typename T>
+__device__ __forceinline__ Raw16<T> load_raw16(const T *p) {
+    return Raw16<T>{load_raw8(p), load_raw8(p + 8)};
+}
+template <typename T>
+__device__ __forceinline__ Raw16<T> zero16();
 template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16 *p, float (&x)[16]) {
-    const Raw8<__nv_bfloat16> a = load_raw8(p), b = load_raw8(p + 8);
+__device__ __forceinline__ Raw16<__nv_bfloat16> zero16<__nv_bfloat16>() {
+    return Raw16<__nv_bfloat16>{{make_uint4(0, 0, 0, 0)}, {make_uint4(0, 0, 0, 0)}};
+}
+template <>
+__device__ __forceinline__ Raw16<float> zero16<float>() {
+    const float4 z = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    return Raw16<float>{{z, z}, {z, z}};
+}
+template <typename T>
+__device__ __forceinline__ void unpack16(const Raw16<T> &r, float (&x)[16]) {
     float u[8], v[8];
-    unpack8(a, u);
-    unpack8(b, v);
+    unpack8(r.a, u);
+    unpack8(r.b, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         x[j] = u[j];
         x[8 + j] = v[j];
     }
 }
-template <>
-__device__ __forceinline__ void load16<float>(const float *p, float (&x)[16]) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float4 v = __ldg(reinterpret_cast<const float4 *>(p) + q);
-        x[4 * q] = v.x;
-        x[4 * q + 1] = v.y;
-        x[4 * q + 2] = v.z;
-        x[4 * q + 3] = v.w;
-    }
+template <typename T>
+__device__ __forceinline__ void load16(const T *p, float (&x)[16]) {
+    unpack16(load_raw16(p), x);
 }
 
 // The place of the scale of row r, block j (fp4 scale tiles: 128 rows by 4 blocks).
