@@ -1023,22 +1023,24 @@ eqat_status eqat_fp4_linear_bwd(const void *X, const uint8_t *codes, const uint8
     }
     const bool nv = fmt == EQAT_FP4_NV;
     uint8_t *w_hat = static_cast<uint8_t *>(ws), *x_hat = w_hat + up256(static_cast<size_t>(N * K) * 2);
+    // both contractions in one grouped launch: the tiles of one fill the last wave of the other
+    eqat::GemmProblem probs[2];
+    int np = 0;
     EpiArgs epi;
     epi.kind = Epi::kStore;
     epi.ldo = K;
     if (dX) {
         EQAT_CUDA(eqat::launch_dequant_fp4(codes, scales, nv, gw, N, K, w_hat, false, dev, st), "fp4 values of W");
         epi.out = dX;
-        EQAT_CUDA(eqat::launch_gemm_tc(Operand{dY, N, false}, Operand{w_hat, K, true}, M, K, N, epi, dev, st),
-                  "fp4 input gradient");
+        probs[np++] = eqat::GemmProblem{Operand{dY, N, false}, Operand{w_hat, K, true}, M, K, N, epi};
     }
     if (dW) {
         EQAT_CUDA(eqat::launch_encode_fp4(X, false, nv, gx, M, K, nullptr, nullptr, x_hat, dev, st),
                   "fp4 values of X");
         epi.out = dW;
-        EQAT_CUDA(eqat::launch_gemm_tc(Operand{dY, N, true}, Operand{x_hat, K, true}, N, K, M, epi, dev, st),
-                  "fp4 weight gradient");
+        probs[np++] = eqat::GemmProblem{Operand{dY, N, true}, Operand{x_hat, K, true}, N, K, M, epi};
     }
+    EQAT_CUDA(eqat::launch_gemm_tc_group(probs, np, dev, st), "fp4 backward contractions");
     return EQAT_OK;
 }
 

@@ -1795,8 +1795,8 @@ cudaError_t launch_gemm_tc_group(const GemmProblem *probs, int nprob, const Devi
         }
         switch (probs[0].epi.kind) {
             case Epi::kStore:
-                if (nprob > 1) return cudaErrorInvalidValue;
-                return launch_pair_variant<0, 0, 2>(maps, p, grid, dev.device, st);
+                return sched ? launch_pair_variant<0, 0, 2, 0, 8, 1>(maps, p, grid, dev.device, st, &spec)
+                             : launch_pair_variant<0, 0, 2>(maps, p, grid, dev.device, st);
             case Epi::kFqGrad:
                 // The straight-through epilogue outlasts a main loop 2048 deep with eight
                 // warps (per-tile timestamps on the 70B gate backward: 13.7 us against
@@ -1826,7 +1826,6 @@ cudaError_t launch_gemm_tc_group(const GemmProblem *probs, int nprob, const Devi
     const int grid = std::min(tiles, dev.sm_count);
     switch (probs[0].epi.kind) {
         case Epi::kStore:
-            if (nprob > 1) return cudaErrorInvalidValue;  // two plain contractions: launch separately
             return launch_variant<0, 0, 2>(maps, p, grid, dev.device, st);
         case Epi::kFqGrad:
             return launch_variant<1, 0, 2>(maps, p, grid, dev.device, st);
