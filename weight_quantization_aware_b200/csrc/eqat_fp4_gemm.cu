@@ -562,19 +562,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             const int row0 = tm * 256 + static_cast<int>(rank) * 128 + quad * 32;
             const bool odd = local & 1u;
             const uint32_t taddr = tmem + ((quad * 32) << 16) + (odd ? kAcc1 : 0);
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i, ++chunk) {
-                // the columns that the next tile's accumulator overlaps come first
-                const int c0 = 32 * (odd ? i : (i + kAcc1 / 32) & 7);
-                float v[32];
-                tmem_ld_32cols(taddr + c0, v);
-                if (i == kOverlap / 32 - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(acc_free0);
-                }
-                // 32 rows of 64 bytes, 16-byte units swizzled as the output map's box
-                uint8_t *dst = buf + (chunk & 1) * 2048;
+            // 32 rows of 64 bytes, 16-byte units swizzled as the output map's box
+            auto put = [&](const float *v, int c0) {
+                uint8_t *dst = buf + (chunk++ & 1) * 2048;
                 if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                 __syncwarp();
 #pragma unroll
@@ -590,6 +580,23 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                 __syncwarp();
                 // the map clips a chunk at the matrix's end
                 if (lane == 0 && row0 < p.rows_a && tn * 256 + c0 < p.rows_b) tma_store_2d(&tmY, dst, tn * 256 + c0, row0);
+            };
+            // The columns that the next tile's accumulator overlaps go to registers first,
+            // and its MMAs may start; then they are written, and the rest follows.
+            const int first = odd ? 0 : kAcc1, rest = odd ? kOverlap : 0;
+            float head[kOverlap / 32][32];
+#pragma unroll
+            for (int i = 0; i < kOverlap / 32; ++i) tmem_ld_32cols(taddr + first + 32 * i, head[i]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_free0);
+#pragma unroll
+            for (int i = 0; i < kOverlap / 32; ++i) put(head[i], first + 32 * i);
+#pragma unroll 1
+            for (int i = 0; i < kAcc1 / 32; ++i) {
+                float v[32];
+                tmem_ld_32cols(taddr + rest + 32 * i, v);
+                put(v, rest + 32 * i);
             }
         }
         if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
