@@ -36,16 +36,26 @@
 namespace eqat {
 namespace {
 
-constexpr int kThreads = 256;  // threads that walk a row
-constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;                           // 16-byte vectors per thread and chunk
-constexpr int kChunk = kThreads * kUnroll;           // vectors of a chunk: 16 KB
-constexpr int kStages = 3;                           // chunks of the ring
-constexpr size_t kRingBytes = static_cast<size_t>(kStages) * kChunk * 16;
-constexpr int kCtasPerSm = 3;
+// W, the template parameter of most functions here, is the number of threads that walk a
+// row: 256 with three blocks per SM, or 768 in one block where there are no more long
+// rows than SMs.  On 8 rows of 131072 bf16 the wide block takes 17.4 us where the narrow
+// one takes 23.8 (distillation step) and 9.0 against 11.1 (log probabilities); on rows of
+// 32000 they are even (9.4 and 9.6, 5.2 and 4.5), on shorter ones the narrow one wins.
+// With alternatives the narrow block does: its bound has fewer maxima to rank (22.7
+// against 17.3 us on those rows).
+constexpr int kWalk = 256, kWalkWide = 768;
+constexpr int kUnroll = 4;  // 16-byte vectors per thread and chunk
+constexpr int kStages = 3;  // chunks of the ring
+template <int W>
+constexpr int kChunk = W * kUnroll;  // vectors of a chunk: 16 KB, or 48 KB
+template <int W>
+constexpr size_t kRingBytes = static_cast<size_t>(kStages) * kChunk<W> * 16;
+template <int W>
+constexpr int kCtasPerSm = W == kWalk ? 3 : 1;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;     // far above any legitimate wait
 constexpr int kNotes = 256;        // vectors that a warp notes for the top-k selection, in shared memory
 constexpr int kKept = 1024;        // entries among them that are ranked
+constexpr size_t kWideBitBytes = 64 * 1024;  // bitmaps beside the wide ring: V up to 262000
 constexpr float kFloor = -1e30f;   // below every logit that has a part in its row
 constexpr uint32_t kNegInfBf16x2 = 0xFF80FF80u;
 constexpr uint32_t kNegInfF32 = 0xFF800000u;
@@ -322,28 +332,29 @@ struct RingPos {
     }
 };
 
+template <int W>
 __device__ __forceinline__ void ring_init(RingCtl &ctl) {
     for (int i = 0; i < kStages; ++i) {
         mbar_init(&ctl.full[i], 1);
-        mbar_init(&ctl.empty[i], kWarps);
+        mbar_init(&ctl.empty[i], W / 32);
     }
     ctl.abort_flag = 0;
     fence_mbarrier_init();
 }
 
-template <typename T>
+template <int W, typename T>
 __device__ __forceinline__ int chunks_of(const Row<T> &row) {
-    return (row.b1 - row.b0 + kChunk - 1) / kChunk;
+    return (row.b1 - row.b0 + kChunk<W> - 1) / kChunk<W>;
 }
 
 // One thread: the row's chunks, once; `again`: they will be read a second time, so L2 is
 // to keep them, and otherwise to let them go first.  A wait that runs out raises the block's abort
 // flag, after which every wait returns at once: the block runs to its end on what the
 // ring holds, and the device error word tells.
-template <typename T>
+template <int W, typename T>
 __device__ __forceinline__ void ring_fill(const Row<T> &row, uint4 *ring, RingCtl &ctl, RingPos &pos, int *err,
                                           bool again) {
-    const int chunks = chunks_of(row);
+    const int chunks = chunks_of<W>(row);
     uint64_t policy;
     if (again)
         asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
@@ -351,12 +362,12 @@ __device__ __forceinline__ void ring_fill(const Row<T> &row, uint4 *ring, RingCt
         asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
     for (int c = 0; c < chunks; ++c, pos.next()) {
         if (!mbar_wait_bounded(&ctl.empty[pos.stage], pos.phase ^ 1u, &ctl.abort_flag, err, kWaitLimitNs)) return;
-        const int v = row.b0 + c * kChunk;
-        const uint32_t bytes = static_cast<uint32_t>(min(kChunk, row.b1 - v)) * 16u;
+        const int v = row.b0 + c * kChunk<W>;
+        const uint32_t bytes = static_cast<uint32_t>(min(kChunk<W>, row.b1 - v)) * 16u;
         mbar_arrive_expect_tx(&ctl.full[pos.stage], bytes);
         asm volatile(
             "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-                smem_u32(ring + pos.stage * kChunk)),
+                smem_u32(ring + pos.stage * kChunk<W>)),
             "l"(row.vec(v)), "r"(bytes), "r"(smem_u32(&ctl.full[pos.stage])), "l"(policy)
             : "memory");
     }
@@ -372,30 +383,30 @@ __device__ __forceinline__ void ring_end(RingCtl &ctl) {
     }
 }
 
-// The walkers: f(r, v, n) for each chunk, with vectors v, v + kThreads, ... of which the
+// The walkers: f(r, v, n) for each chunk, with vectors v, v + W, ... of which the
 // first n are in the row (the others read as -inf); n is kUnroll, known to the compiler,
 // in whole chunks.
-template <typename T, typename F>
+template <int W, typename T, typename F>
 __device__ __forceinline__ void ring_walk(const Row<T> &row, const uint4 *ring, RingCtl &ctl, RingPos &pos, int *err,
                                           F &&f) {
-    const int tid = threadIdx.x, chunks = chunks_of(row);
+    const int tid = threadIdx.x, chunks = chunks_of<W>(row);
 #pragma unroll 1
     for (int c = 0; c < chunks; ++c, pos.next()) {
         (void)mbar_wait_bounded(&ctl.full[pos.stage], pos.phase, &ctl.abort_flag, err, kWaitLimitNs);
-        const uint4 *src = ring + pos.stage * kChunk + tid;
-        const int v = row.b0 + c * kChunk + tid;
+        const uint4 *src = ring + pos.stage * kChunk<W> + tid;
+        const int v = row.b0 + c * kChunk<W> + tid;
         uint4 r[kUnroll];
-        if (row.b0 + (c + 1) * kChunk <= row.b1) {
+        if (row.b0 + (c + 1) * kChunk<W> <= row.b1) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) r[u] = src[u * kThreads];
+            for (int u = 0; u < kUnroll; ++u) r[u] = src[u * W];
             f(r, v, std::integral_constant<int, kUnroll>());
         } else {
             int n = 0;
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const bool in = v + u * kThreads < row.b1;
+                const bool in = v + u * W < row.b1;
                 n += in;
-                r[u] = in ? src[u * kThreads] : make_uint4(Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill);
+                r[u] = in ? src[u * W] : make_uint4(Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill, Vec<T>::kFill);
             }
             f(r, v, n);
         }
@@ -523,8 +534,8 @@ __device__ __forceinline__ RowSums warp_join(const Sums<ENT> &s, float c) {
 // The sums of W warps (a power of two of entries, of which the first W count), in every thread.
 template <int W, bool ENT>
 __device__ __forceinline__ RowSums warps_join(const RowSums *buf, float c) {
-    constexpr int P = W <= 8 ? 8 : 16;
-    static_assert(W <= 16, "at most sixteen warps");
+    constexpr int P = W <= 8 ? 8 : 32;
+    static_assert(W <= 32, "at most thirty-two warps");
     const int i = threadIdx.x & (P - 1);
     RowSums r{kFloor, 0.0f, 0.0f};
     if (i < W) r = buf[i];
@@ -609,74 +620,76 @@ __device__ __forceinline__ float key_value(uint32_t k) {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
 }
 
+template <int W>
 struct TopShared {
-    int vecs[kWarps][kNotes];  // each warp's vectors with an entry that reached the walk's bound
+    int vecs[W / 32][kNotes];  // each warp's vectors with an entry that reached the walk's bound
     alignas(16) uint64_t kept[kKept];  // entries that reach the row's last bound: key << 32 | ~index
-    uint32_t max_key[kThreads];
+    uint32_t max_key[W];
     double logS;
     float bound;
     int kept_count, overflow;
-    int warp_count[kWarps];
+    int warp_count[W / 32];
 };
 
 // Elements of the row for which pred(key, index) holds, counted over the block.
-template <typename T, typename Pred>
-__device__ __forceinline__ int64_t block_count(const Row<T> &row, TopShared &sh, Pred pred) {
+template <int W, typename T, typename Pred>
+__device__ __forceinline__ int64_t block_count(const Row<T> &row, TopShared<W> &sh, Pred pred) {
     int n = 0;
-    for (int i = threadIdx.x; i < row.V; i += kThreads) {
+    for (int i = threadIdx.x; i < row.V; i += W) {
         const float x = Vec<T>::load(row.base + row.mis + i);
         n += x > -INFINITY && pred(order_key(x), static_cast<uint32_t>(i));
     }
     n = __reduce_add_sync(0xffffffffu, n);
-    bar<kThreads>();
+    bar<W>();
     if ((threadIdx.x & 31) == 0) sh.warp_count[threadIdx.x >> 5] = n;
-    bar<kThreads>();
+    bar<W>();
     int64_t total = 0;
-    for (int w = 0; w < kWarps; ++w) total += sh.warp_count[w];
+    for (int w = 0; w < W / 32; ++w) total += sh.warp_count[w];
     return total;
 }
 
 // The k first entries of a row with too many that reach any simple bound (ties): the
 // k-th key, then the last index of its ties, are found bit by bit with one walk each,
 // and exactly k entries collected.
-template <typename T>
-__device__ __noinline__ void top_k_by_bits(const Row<T> row, int k, TopShared &sh) {
+template <int W, typename T>
+__device__ __noinline__ void top_k_by_bits(const Row<T> row, int k, TopShared<W> &sh) {
     uint32_t key = 0;
     for (int b = 31; b >= 0; --b) {
         const uint32_t cand = key | (1u << b);
-        if (block_count(row, sh, [=](uint32_t q, uint32_t) { return q >= cand; }) >= k) key = cand;
+        if (block_count<W>(row, sh, [=](uint32_t q, uint32_t) { return q >= cand; }) >= k) key = cand;
     }
-    const int64_t need = k - block_count(row, sh, [=](uint32_t q, uint32_t) { return q > key; });
+    const int64_t need = k - block_count<W>(row, sh, [=](uint32_t q, uint32_t) { return q > key; });
     // the largest index bound that still leaves fewer than the needed ties before it
     uint32_t last = 0;
     for (int b = 31; b >= 0; --b) {
         const uint32_t cand = last | (1u << b);
         if (cand <= static_cast<uint32_t>(row.V - 1) &&
-            block_count(row, sh, [=](uint32_t q, uint32_t i) { return q == key && i < cand; }) < need)
+            block_count<W>(row, sh, [=](uint32_t q, uint32_t i) { return q == key && i < cand; }) < need)
             last = cand;
     }
-    bar<kThreads>();
+    bar<W>();
     if (threadIdx.x == 0) sh.kept_count = 0;
-    bar<kThreads>();
-    for (int i = threadIdx.x; i < row.V; i += kThreads) {
+    bar<W>();
+    for (int i = threadIdx.x; i < row.V; i += W) {
         const float x = Vec<T>::load(row.base + row.mis + i);
         const uint32_t q = order_key(x), idx = static_cast<uint32_t>(i);
         if (x > -INFINITY && (q > key || (q == key && idx <= last)))
             sh.kept[atomicAdd(&sh.kept_count, 1)] = (static_cast<uint64_t>(q) << 32) | ~idx;
     }
-    bar<kThreads>();
+    bar<W>();
 }
 
 // A value that at least k entries walked so far reach (-FLT_MAX while there are fewer):
 // the k-th largest of the threads' maxima, to its upper 16 bits, found by one warp with a
 // search on the counts, two bits a step, over the bits in which the maxima differ.
-__device__ __forceinline__ float refresh_bound(float thread_max, int k, TopShared &sh) {
+template <int W>
+__device__ __forceinline__ float refresh_bound(float thread_max, int k, TopShared<W> &sh) {
     sh.max_key[threadIdx.x] = order_key(thread_max);
-    bar<kThreads>();
+    bar<W>();
     if (threadIdx.x < 32) {
-        uint32_t q[kThreads / 32], lo = 0xFFFFFFFFu, hi = 0;
+        uint32_t q[W / 32], lo = 0xFFFFFFFFu, hi = 0;
 #pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) {
+        for (int i = 0; i < W / 32; ++i) {
             q[i] = sh.max_key[threadIdx.x + 32 * i];
             lo = min(lo, q[i]);
             hi = max(hi, q[i]);
@@ -690,7 +703,7 @@ __device__ __forceinline__ float refresh_bound(float thread_max, int k, TopShare
         for (int b = top; b >= 16; b -= 2) {
             uint32_t n = 0;  // how many reach digits 1, 2 and 3, ten bits each (at most 256 do)
 #pragma unroll
-            for (int i = 0; i < kThreads / 32; ++i)
+            for (int i = 0; i < W / 32; ++i)
                 n += (q[i] >= t + (1u << b) ? 1u : 0u) + (q[i] >= t + (2u << b) ? 1u << 10 : 0u) +
                      (q[i] >= t + (3u << b) ? 1u << 20 : 0u);
             n = __reduce_add_sync(0xffffffffu, n);
@@ -701,12 +714,13 @@ __device__ __forceinline__ float refresh_bound(float thread_max, int k, TopShare
         const float v = key_value(t);
         if (threadIdx.x == 0) sh.bound = v > 0.5f * kFloor ? v : -FLT_MAX;
     }
-    bar<kThreads>();
+    bar<W>();
     return sh.bound;
 }
 
 // Notes vector v of the lanes where `hit`, in the warp's list; n is its length.
-__device__ __forceinline__ void note(bool hit, int v, int &n, TopShared &sh) {
+template <int W>
+__device__ __forceinline__ void note(bool hit, int v, int &n, TopShared<W> &sh) {
     const uint32_t hits = __ballot_sync(0xffffffffu, hit);
     if (hits) {
         const int lane = threadIdx.x & 31, at = n + __popc(hits & ((1u << lane) - 1u));
@@ -716,8 +730,8 @@ __device__ __forceinline__ void note(bool hit, int v, int &n, TopShared &sh) {
 }
 
 // Entries of vector v that reach the bound, to the kept ones.
-template <typename T>
-__device__ __forceinline__ void keep(const Row<T> &row, const uint4 &r, int v, float bound, TopShared &sh) {
+template <int W, typename T>
+__device__ __forceinline__ void keep(const Row<T> &row, const uint4 &r, int v, float bound, TopShared<W> &sh) {
     uint32_t hits = 0;
 #pragma unroll
     for (int j = 0; j < Vec<T>::N; ++j) hits |= Vec<T>::value(r, j) >= bound ? 1u << j : 0u;  // NaN and -inf never do
@@ -731,33 +745,33 @@ __device__ __forceinline__ void keep(const Row<T> &row, const uint4 &r, int v, f
 // The walk for the sums, which also notes the vectors that may hold alternatives: those
 // with an entry that reaches a bound, refreshed when 1, 4, 16, ... chunks are walked and
 // after the last.  For a row in random order these are about 4 k log4(chunks) vectors.
-template <typename T>
+template <int W, typename T>
 __device__ __forceinline__ Sums<true> walk_candidates(const Row<T> &row, const LogprobArgs &a, const uint4 *ring,
-                                                      RingCtl &ctl, RingPos &pos, TopShared &sh, int &notes) {
+                                                      RingCtl &ctl, RingPos &pos, TopShared<W> &sh, int &notes) {
     Sums<true> s(a.c);
     if (threadIdx.x == 0) sh.kept_count = sh.overflow = 0;
     notes = 0;
     float bound = -FLT_MAX;
     int ve, done = 0, next = 1;
-    const int chunks = chunks_of(row);
+    const int chunks = chunks_of<W>(row);
     const bool edge = row.edge(ve);
     if (edge) {
         uint4 r[1] = {row.load_edge(ve)};
         s.template add<T, 1>(r, a.c);
     }
-    ring_walk(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int) {
+    ring_walk<W>(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int) {
         const float mx = s.template add<T, kUnroll>(r, a.c);
         if (++done == next) {
-            bound = refresh_bound(s.m, a.k, sh);
+            bound = refresh_bound<W>(s.m, a.k, sh);
             next = min(4 * next, chunks);
         }
         if (__any_sync(0xffffffffu, mx >= bound)) {
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) note(Vec<T>::max(r[u]) >= bound, v + u * kThreads, notes, sh);
+            for (int u = 0; u < kUnroll; ++u) note<W>(Vec<T>::max(r[u]) >= bound, v + u * W, notes, sh);
         }
     });
-    if (done == 0) bound = refresh_bound(s.m, a.k, sh);  // a row within two vectors
-    note(edge, ve, notes, sh);
+    if (done == 0) bound = refresh_bound<W>(s.m, a.k, sh);  // a row within two vectors
+    note<W>(edge, ve, notes, sh);
     if (notes > kNotes) sh.overflow = 1;
     return s;
 }
@@ -765,29 +779,29 @@ __device__ __forceinline__ Sums<true> walk_candidates(const Row<T> &row, const L
 // The k largest (value, lowest index first) of a row without NaN or +inf, from the
 // vectors noted in its walk: their entries that reach the row's last bound are ranked by
 // counting.
-template <typename T>
+template <int W, typename T>
 __device__ __forceinline__ void top_k(const Row<T> &row, const LogprobArgs &a, int64_t t, float m, int notes,
-                                      TopShared &sh) {
+                                      TopShared<W> &sh) {
     const int tid = threadIdx.x, k = a.k;
     const float bound = sh.bound;  // the walk's last; the barrier of the sums ended its notes
     if (sh.overflow) {  // a row that rises along the walk: walked again, by the last bound
-        walk_body<kThreads, kUnroll>(row, [&](uint4(&r)[kUnroll], int v, int) {
+        walk_body<W, kUnroll>(row, [&](uint4(&r)[kUnroll], int v, int) {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u)
-                if (Vec<T>::max(r[u]) >= bound) keep(row, r[u], v + u * kThreads, bound, sh);
+                if (Vec<T>::max(r[u]) >= bound) keep<W>(row, r[u], v + u * W, bound, sh);
         });
         int ve;
-        if (row.edge(ve)) keep(row, row.load_edge(ve), ve, bound, sh);
+        if (row.edge(ve)) keep<W>(row, row.load_edge(ve), ve, bound, sh);
     } else {
         for (int i = tid & 31; i < notes; i += 32) {
             const int v = sh.vecs[tid >> 5][i];
-            keep(row, v >= row.b0 && v < row.b1 ? load_vec(row.vec(v)) : row.load_edge(v), v, bound, sh);
+            keep<W>(row, v >= row.b0 && v < row.b1 ? load_vec(row.vec(v)) : row.load_edge(v), v, bound, sh);
         }
     }
-    bar<kThreads>();
-    if (sh.kept_count > kKept) top_k_by_bits(row, k, sh);
+    bar<W>();
+    if (sh.kept_count > kKept) top_k_by_bits<W>(row, k, sh);
     const int n = sh.kept_count;
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < n; i += W) {
         const uint64_t mine = sh.kept[i];
         int rank = 0;
         int j = 0;
@@ -803,19 +817,19 @@ __device__ __forceinline__ void top_k(const Row<T> &row, const LogprobArgs &a, i
             a.top_logprobs[t * k + rank] = static_cast<float>((static_cast<double>(x) - m) * a.inv_tau - sh.logS);
         }
     }
-    for (int i = n + tid; i < k; i += kThreads) {
+    for (int i = n + tid; i < k; i += W) {
         a.top_ids[t * k + i] = -1;
         a.top_logprobs[t * k + i] = -INFINITY;
     }
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) k_token_logprobs(const LogprobArgs a) {
+template <typename T, bool TOP, int W>
+__global__ void __launch_bounds__(W + 32, kCtasPerSm<W>) k_token_logprobs(const LogprobArgs a) {
     extern __shared__ __align__(128) uint4 ring[];
-    __shared__ RowSums buf[2][kWarps];  // in turn, so that a row's readers need no barrier before the next row
+    __shared__ RowSums buf[2][W / 32];  // in turn, so that a row's readers need no barrier before the next row
     __shared__ RingCtl ctl;
-    __shared__ typename std::conditional<TOP, TopShared, int>::type sh;
-    if (threadIdx.x == 0) ring_init(ctl);
+    __shared__ typename std::conditional<TOP, TopShared<W>, int>::type sh;
+    if (threadIdx.x == 0) ring_init<W>(ctl);
     __syncthreads();
     pdl_wait();
     pdl_allow_dependents();
@@ -823,9 +837,9 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) k_token_logprobs(co
     auto row_of = [&](int64_t t) {
         return Row<T>(const_cast<T *>(static_cast<const T *>(a.x)) + t * a.ld, static_cast<int>(a.V));
     };
-    if (threadIdx.x >= kThreads) {
-        if (threadIdx.x == kThreads) {
-            for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) ring_fill(row_of(t), ring, ctl, pos, a.err, false);
+    if (threadIdx.x >= W) {
+        if (threadIdx.x == W) {
+            for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) ring_fill<W>(row_of(t), ring, ctl, pos, a.err, false);
             ring_end(ctl);
         }
         return;
@@ -841,10 +855,10 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) k_token_logprobs(co
         int notes = 0;
         const Sums<true> mine = [&] {
             if constexpr (TOP) {
-                return walk_candidates(row, a, ring, ctl, pos, sh, notes);
+                return walk_candidates<W>(row, a, ring, ctl, pos, sh, notes);
             } else {
                 Sums<true> s(a.c);
-                ring_walk(row, ring, ctl, pos, a.err,
+                ring_walk<W>(row, ring, ctl, pos, a.err,
                           [&](uint4(&r)[kUnroll], int, int) { s.template add<T, kUnroll>(r, a.c); });
                 int v;
                 if (row.edge(v)) {
@@ -854,13 +868,13 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) k_token_logprobs(co
                 return s;
             }
         }();
-        const RowSums w = warp_join(mine, a.c);
-        if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = w;
-        bar<kThreads>();
-        RowSums s = warps_join<kWarps, true>(buf[turn], a.c);
+        const RowSums of_warp = warp_join(mine, a.c);
+        if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = of_warp;
+        bar<W>();
+        RowSums s = warps_join<W / 32, true>(buf[turn], a.c);
         if (is_far(s)) {
-            bar<kThreads>();
-            s = far_sums<kThreads>(row, a.c, buf[turn], [](int) { return true; });
+            bar<W>();
+            s = far_sums<W>(row, a.c, buf[turn], [](int) { return true; });
         }
         const bool none = s.S == 0.0f, bad = !(s.S < INFINITY);
         if (threadIdx.x < 32) {
@@ -882,14 +896,14 @@ __global__ void __launch_bounds__(kThreads + 32, kCtasPerSm) k_token_logprobs(co
         }
         if constexpr (TOP) {
             if (bad || none) {
-                for (int i = threadIdx.x; i < a.k; i += kThreads) {
+                for (int i = threadIdx.x; i < a.k; i += W) {
                     a.top_ids[t * a.k + i] = -1;
                     a.top_logprobs[t * a.k + i] = bad ? NAN : -INFINITY;
                 }
             } else {
-                top_k(row, a, t, s.m, notes, sh);
+                top_k<W>(row, a, t, s.m, notes, sh);
             }
-            bar<kThreads>();  // the next row's walk clears the counts
+            bar<W>();  // the next row's walk clears the counts
         }
     }
 }
@@ -1109,33 +1123,33 @@ __device__ void finish_slots(const DistillArgs &a, Slots &sl, const RowSums &s, 
     __syncwarp();
 }
 
-template <typename T>
+template <int W, typename T>
 __device__ __forceinline__ void zero_row(const Row<T> &out) {
-    for (int v = out.b0 + threadIdx.x; v < out.b1; v += kThreads)
+    for (int v = out.b0 + threadIdx.x; v < out.b1; v += W)
         *const_cast<uint4 *>(out.vec(v)) = make_uint4(0, 0, 0, 0);
     int v;
     if (out.edge(v)) out.store_edge(v, make_uint4(0, 0, 0, 0));
 }
 
-// Warps 0..7 walk; warp 8 looks after the slots: while the others walk a row for its
+// The first W threads walk; the next warp looks after the slots: while the others walk a row for its
 // sums it prepares the next row's, and while they walk it again for the gradient it works
 // out the loss and the gradient at the slots, which it writes when they have passed.
-// Warp 9 fills the ring.
-template <typename T, bool TAIL>
-__global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const DistillArgs a) {
+// The last warp fills the ring.
+template <typename T, bool TAIL, int W>
+__global__ void __launch_bounds__(W + 64, kCtasPerSm<W>) k_distill(const DistillArgs a) {
     extern __shared__ __align__(128) uint4 ring[];
     // two rows': a bit per element of the row's vectors, set on slots
-    uint32_t *bitmaps = reinterpret_cast<uint32_t *>(ring + kStages * kChunk);
-    constexpr int P = kThreads + 32;  // walkers and slot warp
+    uint32_t *bitmaps = reinterpret_cast<uint32_t *>(ring + kStages * kChunk<W>);
+    constexpr int P = W + 32;  // walkers and slot warp
     __shared__ RowSums buf[2][P / 32];
     __shared__ Slots slots[2];
     __shared__ RawSlots raw[2];  // of odd and even rows
     __shared__ RingCtl ctl;
     const int tid = threadIdx.x;
-    const bool walker = tid < kThreads;
+    const bool walker = tid < W;
     const int words = static_cast<int>((a.V + Vec<T>::N + 31) / 32);
-    for (int i = tid; i < 2 * words; i += kThreads + 64) bitmaps[i] = 0;
-    if (tid == 0) ring_init(ctl);
+    for (int i = tid; i < 2 * words; i += W + 64) bitmaps[i] = 0;
+    if (tid == 0) ring_init<W>(ctl);
     __syncthreads();
     pdl_wait();
     pdl_allow_dependents();
@@ -1147,8 +1161,8 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const Dis
         if (tid == P) {
             for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
                 if (a.weight && a.weight[t] == 0.0f) continue;
-                ring_fill(row_of(a.x, t), ring, ctl, pos, a.err, a.dx != nullptr);
-                if (a.dx) ring_fill(row_of(a.x, t), ring, ctl, pos, a.err, false);
+                ring_fill<W>(row_of(a.x, t), ring, ctl, pos, a.err, a.dx != nullptr);
+                if (a.dx) ring_fill<W>(row_of(a.x, t), ring, ctl, pos, a.err, false);
             }
             ring_end(ctl);
         }
@@ -1182,11 +1196,11 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const Dis
                 const uint32_t bits = (bitmap[at >> 5] >> (at & 31)) & ((1u << Vec<T>::N) - 1u);
                 if (bits) Vec<T>::fill(r, bits);
             };
-            ring_walk(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int n) {
+            ring_walk<W>(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int n) {
                 if (TAIL) {
 #pragma unroll
                     for (int u = 0; u < kUnroll; ++u)
-                        if (u < n) mask(r[u], v + u * kThreads);
+                        if (u < n) mask(r[u], v + u * W);
                 }
                 mine.template add<T, kUnroll>(r, a.c);
             });
@@ -1208,7 +1222,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const Dis
         RowSums s;
         RowState st;
         if (!skip) {
-            s = warps_join<kWarps, false>(buf[turn], a.c);
+            s = warps_join<W / 32, false>(buf[turn], a.c);
             if (is_far(s)) {
                 bar<P>();
                 s = far_sums<P>(row, a.c, buf[turn], [&](int e) {
@@ -1223,7 +1237,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const Dis
         if (walker) {
             if (a.dx) {
                 if (skip) {
-                    zero_row(out);
+                    zero_row<W>(out);
                 } else {
                     const uint64_t nm = f2_pack(-s.m, -s.m), c2 = f2_pack(a.c, a.c), k2 = f2_pack(st.coef, st.coef);
                     auto grad = [&](const uint4 &r) {
@@ -1238,11 +1252,11 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const Dis
                         return Vec<T>::from_pairs(e);
                     };
                     const bool zero = st.zero;
-                    ring_walk(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int n) {
+                    ring_walk<W>(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int n) {
 #pragma unroll
                         for (int u = 0; u < kUnroll; ++u)
                             if (u < n)
-                                __stcs(const_cast<uint4 *>(out.vec(v + u * kThreads)),
+                                __stcs(const_cast<uint4 *>(out.vec(v + u * W)),
                                        zero ? make_uint4(0, 0, 0, 0) : grad(r[u]));
                     });
                     int ve;
@@ -1250,7 +1264,7 @@ __global__ void __launch_bounds__(kThreads + 64, kCtasPerSm) k_distill(const Dis
                 }
             }
         } else if (skip) {
-            if (tid == kThreads && a.loss) a.loss[t] = 0.0f;
+            if (tid == W && a.loss) a.loss[t] = 0.0f;
         } else {
             finish_slots<TAIL>(a, sl, s, st, t);
         }
@@ -1277,17 +1291,55 @@ cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t> &done, const 
     return e;
 }
 
-}  // namespace
-
-template <typename T, bool TOP>
-static cudaError_t launch_logprobs_t(const LogprobArgs &a, const DeviceInfo &dev, cudaStream_t st) {
+template <typename T, bool TOP, int W>
+cudaError_t launch_logprobs_w(const LogprobArgs &a, const DeviceInfo &dev, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
-    auto kern = k_token_logprobs<T, TOP>;
-    cudaError_t e = allow_smem(kern, kRingBytes, done, dev);
+    auto kern = k_token_logprobs<T, TOP, W>;
+    cudaError_t e = allow_smem(kern, kRingBytes<W>, done, dev);
     if (e != cudaSuccess) return e;
-    const int grid = static_cast<int>(std::min<int64_t>(a.T, static_cast<int64_t>(dev.sm_count) * kCtasPerSm));
-    return launch_pdl(kern, dim3(grid), dim3(kThreads + 32), kRingBytes, st, a);
+    const int grid = static_cast<int>(std::min<int64_t>(a.T, static_cast<int64_t>(dev.sm_count) * kCtasPerSm<W>));
+    return launch_pdl(kern, dim3(grid), dim3(W + 32), kRingBytes<W>, st, a);
 }
+
+// Rows for the wide block: no more than SMs, and long (see kWalkWide).
+inline bool few_long_rows(int64_t T, int64_t row_bytes, const DeviceInfo &dev) {
+    return T <= dev.sm_count && row_bytes >= 128 * 1024;
+}
+
+template <typename T>
+cudaError_t launch_logprobs_t(const LogprobArgs &a, const DeviceInfo &dev, cudaStream_t st) {
+    if (a.k > 0) return launch_logprobs_w<T, true, kWalk>(a, dev, st);
+    return few_long_rows(a.T, a.V * static_cast<int64_t>(sizeof(T)), dev) ? launch_logprobs_w<T, false, kWalkWide>(a, dev, st)
+                                                                          : launch_logprobs_w<T, false, kWalk>(a, dev, st);
+}
+
+template <typename T, bool TAIL, int W>
+cudaError_t launch_distill_w(const DistillArgs &a, const DeviceInfo &dev, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    auto kern = k_distill<T, TAIL, W>;
+    // two bits per vocabulary entry: the wide block's ring leaves room for fewer entries
+    const size_t bits = static_cast<size_t>((a.V + Vec<T>::N + 31) / 32) * 8;
+    constexpr size_t most = W == kWalk ? static_cast<size_t>((kDistillMaxV + 64) / 4) : kWideBitBytes;
+    cudaError_t e = allow_smem(kern, kRingBytes<W> + most, done, dev);
+    if (e != cudaSuccess) return e;
+    // The rows that are walked twice at a time have to stay in the 126 MB L2 beside what
+    // is written: 2048 rows of 131072 bf16 take 207 us with two blocks per SM, 240 us with
+    // three and 278 us with one.
+    const int64_t row_bytes = a.V * static_cast<int64_t>(sizeof(T)) * dev.sm_count;
+    const int64_t per_sm =
+        std::max<int64_t>(1, std::min<int64_t>(kCtasPerSm<W>, (80ll << 20) / std::max<int64_t>(row_bytes, 1)));
+    const int grid = static_cast<int>(std::min<int64_t>(a.T, dev.sm_count * per_sm));
+    return launch_pdl(kern, dim3(grid), dim3(W + 64), kRingBytes<W> + bits, st, a);
+}
+
+template <typename T, bool TAIL>
+cudaError_t launch_distill_t(const DistillArgs &a, const DeviceInfo &dev, cudaStream_t st) {
+    const size_t bits = static_cast<size_t>((a.V + Vec<T>::N + 31) / 32) * 8;
+    const bool wide = few_long_rows(a.T, a.V * static_cast<int64_t>(sizeof(T)), dev) && bits <= kWideBitBytes;
+    return wide ? launch_distill_w<T, TAIL, kWalkWide>(a, dev, st) : launch_distill_w<T, TAIL, kWalk>(a, dev, st);
+}
+
+}  // namespace
 
 cudaError_t launch_token_logprobs(const void *x, bool f32, int64_t ld, int64_t T, int64_t V, const int64_t *targets,
                                   double temperature, int k, float *logprob, float *entropy, int64_t *top_ids,
@@ -1295,23 +1347,7 @@ cudaError_t launch_token_logprobs(const void *x, bool f32, int64_t ld, int64_t T
     LogprobArgs a{x, ld, T, V, targets, static_cast<float>(1.44269504088896340736 / temperature), 1.0 / temperature,
                   k, logprob, entropy, top_ids, top_logprobs, device_error_word()};
     if (!a.err) return cudaErrorInvalidSymbol;
-    if (f32) return k ? launch_logprobs_t<float, true>(a, dev, st) : launch_logprobs_t<float, false>(a, dev, st);
-    return k ? launch_logprobs_t<__nv_bfloat16, true>(a, dev, st) : launch_logprobs_t<__nv_bfloat16, false>(a, dev, st);
-}
-
-template <typename T, bool TAIL>
-static cudaError_t launch_distill_t(const DistillArgs &a, const DeviceInfo &dev, cudaStream_t st) {
-    static std::atomic<uint64_t> done{0};
-    auto kern = k_distill<T, TAIL>;
-    cudaError_t e = allow_smem(kern, kRingBytes + static_cast<size_t>((kDistillMaxV + 64) / 4), done, dev);
-    if (e != cudaSuccess) return e;
-    const size_t smem = kRingBytes + static_cast<size_t>((a.V + Vec<T>::N + 31) / 32) * 8;
-    // The rows that are walked twice at a time have to stay in the 126 MB L2 beside what
-    // is written.
-    const int64_t row_bytes = a.V * static_cast<int64_t>(sizeof(T)) * dev.sm_count;
-    const int64_t per_sm = std::max<int64_t>(1, std::min<int64_t>(kCtasPerSm, (80ll << 20) / std::max<int64_t>(row_bytes, 1)));
-    const int grid = static_cast<int>(std::min<int64_t>(a.T, dev.sm_count * per_sm));
-    return launch_pdl(kern, dim3(grid), dim3(kThreads + 64), smem, st, a);
+    return f32 ? launch_logprobs_t<float>(a, dev, st) : launch_logprobs_t<__nv_bfloat16>(a, dev, st);
 }
 
 cudaError_t launch_distill_topk(const void *x, bool f32, int64_t ld, int64_t T, int64_t V, const int64_t *ids,
