@@ -27,6 +27,9 @@ EQAT_TOP_MAX = 128  # alternatives per row of token_logprobs and distill_topk_*
 EQAT_ERR_TIMEOUT = 8
 
 _lib = None
+# the raw handle of torch.cuda.current_stream(dev), without making a Stream object (3 us)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 class EqatError(RuntimeError):
@@ -115,8 +118,7 @@ def _p(t):
 
 
 def _stream():
-    # the raw handle of torch.cuda.current_stream(), without making a Stream object (3 us)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _dt(t: torch.Tensor) -> int:
@@ -507,9 +509,11 @@ def fq_linear_fwd_mse(X, W, s, z, T, bits, group, ws=None, dY=None, loss=None):
 
 def _arg(t, name, dtype, shape, dev):
     """The pointer of a dense CUDA tensor of this dtype and shape on device `dev`."""
-    if (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.is_cuda and t.is_contiguous()
-            and t.get_device() == dev):
-        return t.data_ptr()
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     _shape(t, name, shape)
     _req(t, name, dtype)
     raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
@@ -525,9 +529,14 @@ def _check(fn, st):
 
 
 def _enter():
-    """(library, current device, raw handle of its current stream)."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -1
-    return _lib or load_library(), dev, torch._C._cuda_getCurrentRawStream(dev) if dev >= 0 else None
+    """(library, current device, raw handle of its current stream); device -2 where there
+    is no CUDA device (no tensor is on it)."""
+    if _lib is None:
+        load_library()
+    if not (torch.cuda.is_initialized() or torch.cuda.is_available()):
+        return _lib, -2, None
+    dev = torch.cuda.current_device()
+    return _lib, dev, _raw_stream(dev)
 
 
 def _rows(x, name, dev):
@@ -542,8 +551,6 @@ def _rows(x, name, dev):
         ld = V
     if (V > 1 and sv != 1) or ld < V:
         raise ValueError(f"{name} must have dense rows that do not overlap, got strides {x.stride()}")
-    if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     if x.get_device() != dev:
         raise ValueError(f"{name} is on {x.device}, the current device is cuda:{dev}")
     return T, V, ld
@@ -558,12 +565,10 @@ def token_logprobs(logits, targets, top_k=0, temperature=1.0):
     lib, dev, stream = _enter()
     T, V, ld = _rows(logits, "logits", dev)
     tp = _arg(targets, "targets", torch.int64, (T,), dev)
-    where = logits.device
     lp, ent = torch.empty_like(targets, dtype=torch.float32), torch.empty_like(targets, dtype=torch.float32)
     ids = top = None
     if top_k > 0:
-        ids = torch.empty((T, top_k), dtype=torch.int64, device=where)
-        top = torch.empty((T, top_k), dtype=torch.float32, device=where)
+        ids, top = targets.new_empty(T, top_k), lp.new_empty(T, top_k)
     _check("eqat_token_logprobs", lib.eqat_token_logprobs(
         logits.data_ptr(), _dt(logits), ld, T, V, tp, temperature, top_k, lp.data_ptr(), ent.data_ptr(),
         ids.data_ptr() if top_k > 0 else None, top.data_ptr() if top_k > 0 else None, stream))
@@ -578,11 +583,10 @@ def _distill(logits, ids, tlp, weight, temperature, tail, want_loss, want_grad, 
     k = ids.shape[1]
     ip, tp = _arg(ids, "ids", torch.int64, (T, k), dev), _arg(tlp, "tlp", torch.float32, (T, k), dev)
     wp = _opt(weight, "weight", torch.float32, (T,), dev)
-    where = logits.device
     gp = None
     if want_grad:
         if dlogits is None:
-            dlogits = torch.empty((T, ld), dtype=logits.dtype, device=where)
+            dlogits = logits.new_empty(T, ld)
             dlogits = dlogits if ld == V else dlogits[:, :V]
         else:
             _shape(dlogits, "dlogits", (T, V))
@@ -591,7 +595,7 @@ def _distill(logits, ids, tlp, weight, temperature, tail, want_loss, want_grad, 
             if dlogits.dtype != logits.dtype:
                 raise TypeError(f"dlogits must be {logits.dtype}, got {dlogits.dtype}")
         gp = dlogits.data_ptr()
-    loss = torch.empty(T, dtype=torch.float32, device=where) if want_loss else None
+    loss = tlp.new_empty(T) if want_loss else None
     _check("eqat_distill_topk", lib.eqat_distill_topk(
         logits.data_ptr(), _dt(logits), ld, T, V, ip, tp, k, temperature, EQAT_DISTILL_TAIL if tail else 0, wp,
         loss.data_ptr() if want_loss else None, gp, stream))
@@ -659,7 +663,7 @@ def fp4_tensor_scale(W, out=None):
     max|W| <= 6 * 448 * g, one fp32 value on the device."""
     lib, dev, stream = _enter()
     wp = _arg(W, "W", W.dtype, _fp4_matrix(W), dev)
-    out = torch.empty(1, dtype=torch.float32, device=W.device) if out is None else out
+    out = W.new_empty(1, dtype=torch.float32) if out is None else out
     _check("eqat_fp4_tensor_scale", lib.eqat_fp4_tensor_scale(
         wp, _dt(W), W.numel(), _arg(out, "out", torch.float32, (1,), dev), stream))
     return out
@@ -678,9 +682,9 @@ def pack_fp4(W, fmt, tscale=None, codes=None, scales=None):
         _arg(scales, "scales", torch.uint8, sshape, dev)
     wp, gp = _arg(W, "W", W.dtype, (N, K), dev), _opt(tscale, "tscale", torch.float32, (1,), dev)
     if codes is None:
-        codes = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
+        codes = W.new_empty(N, K // 2, dtype=torch.uint8)
     if scales is None:
-        scales = torch.empty(sshape, dtype=torch.uint8, device=W.device)
+        scales = codes.new_empty(*sshape)
     _check("eqat_pack_fp4", lib.eqat_pack_fp4(wp, _dt(W), N, K, f, gp, codes.data_ptr(), scales.data_ptr(), stream))
     return codes, scales
 
@@ -709,7 +713,7 @@ def dequant_fp4(codes, scales, fmt, tscale=None, dtype=torch.bfloat16, out=None)
     sp = _arg(scales, "scales", torch.uint8, fp4_scale_shape(N, K, fmt), dev)
     gp = _opt(tscale, "tscale", torch.float32, (1,), dev)
     if out is None:
-        out = torch.empty((N, K), dtype=dtype, device=codes.device)
+        out = codes.new_empty(N, K, dtype=dtype)
     op = _arg(out, "out", out.dtype, (N, K), dev)
     _check("eqat_dequant_fp4", lib.eqat_dequant_fp4(cp, sp, N, K, f, gp, op, _dt(out), stream))
     return out
@@ -735,7 +739,7 @@ def _fp4_ws(ws, M, N, K, fmt, backward, dev, like):
         n = _lib.eqat_fp4_workspace_bytes(M, N, K, _FP4_FMT[fmt], backward)
         if n == 0:
             return None, None, 0
-        ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+        ws = like.new_empty(n)
         return ws, ws.data_ptr(), n
     return ws, _arg(ws, "ws", torch.uint8, ws.shape, dev), ws.numel()
 
@@ -747,11 +751,11 @@ def fp4_linear_fwd(X, codes, scales, fmt, tscale=None, x_tscale=None, ws=None, Y
     lib, dev, stream = _enter()
     M, N, K, xp, cp, sp, gw, gx = _fp4_operands(X, codes, scales, fmt, tscale, x_tscale, dev)
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
+        Y = X.new_empty(M, N)
         yp = Y.data_ptr()
     else:
         yp = _arg(Y, "Y", torch.bfloat16, (M, N), dev)
-    ws, wp, wn = _fp4_ws(ws, M, N, K, fmt, False, dev, X)
+    ws, wp, wn = _fp4_ws(ws, M, N, K, fmt, False, dev, codes)
     _check("eqat_fp4_linear_fwd", lib.eqat_fp4_linear_fwd(xp, cp, sp, f, gx, gw, yp, M, N, K, wp, wn, stream))
     return Y
 
@@ -765,11 +769,11 @@ def fp4_linear_bwd(X, codes, scales, dY, fmt, tscale=None, x_tscale=None, need_d
     M, N, K, xp, cp, sp, gw, gx = _fp4_operands(X, codes, scales, fmt, tscale, x_tscale, dev)
     dyp = _arg(dY, "dY", torch.bfloat16, (M, N), dev)
     if out is None:
-        dX = torch.empty((M, K), dtype=torch.bfloat16, device=X.device) if need_dx else None
-        dW = torch.empty((N, K), dtype=torch.bfloat16, device=X.device) if need_dw else None
+        dX = X.new_empty(M, K) if need_dx else None
+        dW = X.new_empty(N, K) if need_dw else None
     else:
         dX, dW = out
-    ws, wp, wn = _fp4_ws(ws, M, N, K, fmt, True, dev, X)
+    ws, wp, wn = _fp4_ws(ws, M, N, K, fmt, True, dev, codes)
     _check("eqat_fp4_linear_bwd", lib.eqat_fp4_linear_bwd(
         xp, cp, sp, f, gx, gw, dyp, _opt(dX, "dX", torch.bfloat16, (M, K), dev),
         _opt(dW, "dW", torch.bfloat16, (N, K), dev), M, N, K, wp, wn, stream))
