@@ -679,40 +679,55 @@ __device__ __noinline__ void top_k_by_bits(const Row<T> row, int k, TopShared<W>
     bar<W>();
 }
 
+// The k-th largest of 32 Q keys in shared memory, to its upper 16 bits: a search on the
+// counts, two bits a step, over the bits in which the keys differ.  One warp.
+template <int Q>
+__device__ __forceinline__ uint32_t search_bound(const uint32_t *keys, int k) {
+    uint32_t q[Q], lo = 0xFFFFFFFFu, hi = 0;
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        q[i] = keys[(threadIdx.x & 31) + 32 * i];
+        lo = min(lo, q[i]);
+        hi = max(hi, q[i]);
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    // two-bit digits at 30, 28, .. 16; above `top` all keys agree
+    const int top = (31 - __clz(static_cast<int>((lo ^ hi) | 1u))) & ~1;
+    uint32_t t = top < 30 ? hi & ~((4u << top) - 1u) : 0u;
+#pragma unroll 1
+    for (int b = top; b >= 16; b -= 2) {
+        uint32_t n = 0;  // how many reach digits 1, 2 and 3, ten bits each (at most 256 do)
+#pragma unroll
+        for (int i = 0; i < Q; ++i)
+            n += (q[i] >= t + (1u << b) ? 1u : 0u) + (q[i] >= t + (2u << b) ? 1u << 10 : 0u) +
+                 (q[i] >= t + (3u << b) ? 1u << 20 : 0u);
+        n = __reduce_add_sync(0xffffffffu, n);
+        const uint32_t need = static_cast<uint32_t>(k);
+        t += ((n >> 20) >= need ? 3u : ((n >> 10) & 1023u) >= need ? 2u : (n & 1023u) >= need ? 1u : 0u) << b;
+    }
+    return t;
+}
+
 // A value that at least k entries walked so far reach (-FLT_MAX while there are fewer):
-// the k-th largest of the threads' maxima, to its upper 16 bits, found by one warp with a
-// search on the counts, two bits a step, over the bits in which the maxima differ.
+// the k-th largest of the maxima of the threads, or for small k of groups of 4 or 8 of
+// them (still at least 2 k; for k = 64 pairs gave more candidates than they saved), found
+// by one warp.
 template <int W>
 __device__ __forceinline__ float refresh_bound(float thread_max, int k, TopShared<W> &sh) {
-    sh.max_key[threadIdx.x] = order_key(thread_max);
+    static_assert(W == 256, "keys of 256 threads");
+    const int tid = threadIdx.x, shift = k <= 16 ? 3 : k <= 32 ? 2 : 0;
+    float g = thread_max;
+    for (int i = 0; i < shift; ++i) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1 << i));
+    if ((tid & ((1 << shift) - 1)) == 0) sh.max_key[tid >> shift] = order_key(g);
     bar<W>();
-    if (threadIdx.x < 32) {
-        uint32_t q[W / 32], lo = 0xFFFFFFFFu, hi = 0;
-#pragma unroll
-        for (int i = 0; i < W / 32; ++i) {
-            q[i] = sh.max_key[threadIdx.x + 32 * i];
-            lo = min(lo, q[i]);
-            hi = max(hi, q[i]);
-        }
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        // two-bit digits at 30, 28, .. 16; above `top` all maxima agree
-        const int top = (31 - __clz(static_cast<int>((lo ^ hi) | 1u))) & ~1;
-        uint32_t t = top < 30 ? hi & ~((4u << top) - 1u) : 0u;
-#pragma unroll 1
-        for (int b = top; b >= 16; b -= 2) {
-            uint32_t n = 0;  // how many reach digits 1, 2 and 3, ten bits each (at most 256 do)
-#pragma unroll
-            for (int i = 0; i < W / 32; ++i)
-                n += (q[i] >= t + (1u << b) ? 1u : 0u) + (q[i] >= t + (2u << b) ? 1u << 10 : 0u) +
-                     (q[i] >= t + (3u << b) ? 1u << 20 : 0u);
-            n = __reduce_add_sync(0xffffffffu, n);
-            const uint32_t need = static_cast<uint32_t>(k);
-            t += ((n >> 20) >= need ? 3u : ((n >> 10) & 1023u) >= need ? 2u : (n & 1023u) >= need ? 1u : 0u) << b;
-        }
+    if (tid < 32) {
+        const uint32_t t = shift == 3   ? search_bound<1>(sh.max_key, k)
+                           : shift == 2 ? search_bound<2>(sh.max_key, k)
+                                        : search_bound<8>(sh.max_key, k);
         // a thread without an entry above kFloor says about kFloor: no bound then
         const float v = key_value(t);
-        if (threadIdx.x == 0) sh.bound = v > 0.5f * kFloor ? v : -FLT_MAX;
+        if (tid == 0) sh.bound = v > 0.5f * kFloor ? v : -FLT_MAX;
     }
     bar<W>();
     return sh.bound;
