@@ -119,6 +119,48 @@ def test_logprobs_strides_masks_and_bad_rows(dtype):
         check_logprobs(x, torch.full((T,), -1, device="cuda"), 0)
 
 
+@pytest.mark.parametrize("tau", [1.0, 0.05, 20.0])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_masks_of_every_size(dtype, tau):
+    """Finite masks from -1e4 to the type's lowest value over whole threads' entries, at
+    the front, at the back and alternating, rows of one such value, and rows around
+    it: the sums must come from the entries that are left."""
+    V = 9001
+    masks = [-1e4, -1e7, -1e8, -1e10, -1e15, -1e30, torch.finfo(dtype).min, -float("inf")]
+    x = make(4 * len(masks), V, dtype, 5)
+    for i, m in enumerate(masks):
+        x[4 * i, :8500] = m
+        x[4 * i + 1, 300:] = m
+        x[4 * i + 2, torch.arange(V, device="cuda") % 7 != 3] = m
+        x[4 * i + 3] = m
+        x[4 * i + 3, ::5] = m * (1.01 if abs(m) < 1e37 else 0.99)
+    t = torch.full((len(x),), 8999, device="cuda")
+    xn = f64(x)
+    with np.errstate(invalid="ignore", over="ignore"):
+        zmax = np.where(np.isfinite(xn.max(1)), np.abs(xn.max(1)), 0) / tau
+    lp, ent, ids, top = eqat.token_logprobs(x, t, top_k=12, temperature=tau)
+    w_lp, w_ent, w_ids, w_top = orc.token_logprobs(xn, t.cpu().numpy(), 12, tau)
+    with np.errstate(over="ignore"):  # beyond fp32 a log probability is -inf
+        w_lp, w_top = w_lp.astype(np.float32).astype(np.float64), w_top.astype(np.float32).astype(np.float64)
+    # y = (x - m) c is rounded to 2^-23 of itself, which in a far row may be large where it counts (|y| < 150)
+    e = tol(V) + 2.0 ** -22 * np.minimum(zmax, 100)
+    same(f64(lp), w_lp, e + np.abs(np.nan_to_num(w_lp, neginf=0)) * 2.0 ** -22, "logprob")
+    same(f64(ent), w_ent, e * (2 + 3 * (np.abs(w_ent) + np.log(V))), "entropy")
+    assert np.array_equal(ids.cpu().numpy(), w_ids)
+    same(f64(top), w_top, e[:, None] + np.abs(np.nan_to_num(w_top, neginf=0)) * 2.0 ** -22, "top")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    tids = torch.stack([torch.randperm(V, generator=gen, device="cuda")[:9] for _ in range(len(x))])
+    tlp = torch.log_softmax(torch.randn(len(x), 10, generator=gen, device="cuda"), 1)[:, :9].contiguous()
+    for tail in (False, True):
+        want_l, want_g = orc.distill_topk(xn, tids.cpu().numpy(), f64(tlp), None, tau, tail)
+        loss, grad = eqat.distill_topk_step(x, tids, tlp, temperature=tau, tail=tail)
+        with np.errstate(over="ignore"):
+            want_l = want_l.astype(np.float32).astype(np.float64)
+        same(f64(loss), want_l, 4 * e + np.abs(np.nan_to_num(want_l, posinf=0)) * 2.0 ** -21 + 1e-37, "loss")
+        rel = 4 * e[:, None] + 2.0 ** -19 + 150 * 2.0 ** -23
+        same(f64(grad), want_g, 3 * rel / tau + np.abs(want_g) * HALF[dtype] + 1e-37, "gradient")
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 def test_top_k_of_uneven_and_tied_rows(dtype):
     """Rows whose candidates overflow the selection's buffer: large values in one stride

@@ -7,11 +7,12 @@
 // maximum m, S = sum 2^y and (for the entropy) A = sum 2^y y per thread, with
 // y = (x - m) c and c = log2(e) / temperature.  y is one fma, x c - RN(m c), and what
 // the rounding of m c moved all of a thread's terms by is taken out of S and A at the
-// end (m c - RN(m c) is exact in one fma).  That form needs |x| c far below the fp32
-// range: it starts from m = -1e30, and a row whose S then is 0 or not finite (all
-// entries masked, or at the type's lowest value, or a NaN, an infinity, a value near
-// the type's largest) is walked again with x - m formed first.  The second walk (top
-// alternatives, gradient) reads the row again while it is in L2.
+// end (m c - RN(m c) is exact in one fma).  That form needs |m c| well below 2^31, where
+// RN would move it by more than ex2 can say: m starts from a floor of -2^23 / c, which
+// also keeps masked entries of any kind (-inf, the type's lowest value, -1e10) from being
+// a reference.  A row without an entry above the floor, or whose S is not finite (a NaN,
+// an infinity, values beyond 2^31 / c), is walked again with x - m formed first.  The
+// second walk (top alternatives, gradient) reads the row again while it is in L2.
 //
 // What bounds the first walk besides memory is ex2 (a quarter of the issue rate), then
 // instruction issue: one packed-fp32 instruction does two entries of each step.
@@ -56,7 +57,6 @@ constexpr uint64_t kWaitLimitNs = 4000000000ull;     // far above any legitimate
 constexpr int kNotes = 256;        // vectors that a warp notes for the top-k selection, in shared memory
 constexpr int kKept = 1024;        // entries among them that are ranked
 constexpr size_t kWideBitBytes = 64 * 1024;  // bitmaps beside the wide ring: V up to 262000
-constexpr float kFloor = -1e30f;   // below every logit that has a part in its row
 constexpr uint32_t kNegInfBf16x2 = 0xFF80FF80u;
 constexpr uint32_t kNegInfF32 = 0xFF800000u;
 
@@ -125,10 +125,10 @@ struct Vec<__nv_bfloat16> {
         }
         return fmaxf(__low2float(m), __high2float(m));
     }
-    // entries below kFloor (masked ones) to about kFloor; NaN stays
-    static __device__ __forceinline__ uint4 clamp(uint4 r) {
+    // entries below `low` to about it; NaN stays
+    static __device__ __forceinline__ uint4 clamp(uint4 r, float low) {
         __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&r);
-        const __nv_bfloat162 f = __float2bfloat162_rn(kFloor);
+        const __nv_bfloat162 f = __float2bfloat162_rn(low);
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[i] = __hmax2_nan(h[i], f);
         return r;
@@ -191,10 +191,10 @@ struct Vec<float> {
         for (int u = 1; u < U; ++u) m = fmaxf(m, max(r[u]));
         return m;
     }
-    static __device__ __forceinline__ uint4 clamp(uint4 r) {
+    static __device__ __forceinline__ uint4 clamp(uint4 r, float low) {
         uint32_t *w = reinterpret_cast<uint32_t *>(&r);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(max_nan(__uint_as_float(w[i]), kFloor));
+        for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(max_nan(__uint_as_float(w[i]), low));
         return r;
     }
     static __device__ __forceinline__ void set(uint4 &r, int j, uint32_t raw) {
@@ -443,14 +443,18 @@ __device__ __forceinline__ bool bar_or(bool x) {
 
 // ------------------------------------------------------------------ running softmax sums
 
+// Where the running maximum starts.
+__host__ __device__ __forceinline__ float floor_of(float c) { return -8388608.0f / c; }
+
 // A NaN or +inf entry makes S NaN and stays.
 template <bool ENT>
 struct Sums {
-    float m = kFloor;
+    float m;
     float mu;  // RN(m c), what y is measured from
+    float low;  // 0 times -inf would be NaN in A: entries are raised to here, where 2^y is 0
     uint64_t S = 0, A = 0;  // two partial sums each
 
-    __device__ __forceinline__ explicit Sums(float c) : mu(kFloor * c) {}
+    __device__ __forceinline__ explicit Sums(float c) : m(floor_of(c)), mu(m * c), low(4.0f * m) {}
 
     template <typename T, int U>
     __device__ __forceinline__ float add(const uint4 (&r)[U], float c) {
@@ -467,7 +471,7 @@ struct Sums {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             uint64_t p[Vec<T>::N / 2];
-            Vec<T>::pairs(ENT ? Vec<T>::clamp(r[u]) : r[u], p);  // 0 times -inf would be NaN in A
+            Vec<T>::pairs(ENT ? Vec<T>::clamp(r[u], low) : r[u], p);
 #pragma unroll
             for (int i = 0; i < Vec<T>::N / 2; ++i) {
                 const uint64_t y = f2_fma(p[i], c2, nmu);
@@ -526,8 +530,8 @@ __device__ __forceinline__ RowSums warp_join(const Sums<ENT> &s, float c) {
     f2_unpack(s.S, lo, hi);
     const float S = lo + hi;
     f2_unpack(s.A, lo, hi);
-    r.S = S == 0.0f ? 0.0f : S * f;  // without an entry, kFloor c is rounded by more than ex2 can say
-    r.A = S == 0.0f ? 0.0f : (lo + hi - off_mu * S) * f;
+    r.S = S * f;
+    r.A = (lo + hi - off_mu * S) * f;
     return lanes_join<16, ENT>(r, c);
 }
 
@@ -537,7 +541,7 @@ __device__ __forceinline__ RowSums warps_join(const RowSums *buf, float c) {
     constexpr int P = W <= 8 ? 8 : 32;
     static_assert(W <= 32, "at most thirty-two warps");
     const int i = threadIdx.x & (P - 1);
-    RowSums r{kFloor, 0.0f, 0.0f};
+    RowSums r{-FLT_MAX, 0.0f, 0.0f};
     if (i < W) r = buf[i];
     return lanes_join<P / 2, ENT>(r, c);
 }
@@ -594,7 +598,8 @@ __device__ __noinline__ RowSums far_sums(const Row<T> row, float c, RowSums *buf
     return r;
 }
 
-__device__ __forceinline__ bool is_far(const RowSums &s) { return s.S == 0.0f || !(s.S < INFINITY); }
+// No entry above the floor, or no finite sum.
+__device__ __forceinline__ bool is_far(const RowSums &s, float c) { return s.m <= floor_of(c) || !(s.S < INFINITY); }
 
 // ------------------------------------------------------------------ log probabilities
 
@@ -714,7 +719,7 @@ __device__ __forceinline__ uint32_t search_bound(const uint32_t *keys, int k) {
 // them (still at least 2 k; for k = 64 pairs gave more candidates than they saved), found
 // by one warp.
 template <int W>
-__device__ __forceinline__ float refresh_bound(float thread_max, int k, TopShared<W> &sh) {
+__device__ __forceinline__ float refresh_bound(float thread_max, int k, float floor, TopShared<W> &sh) {
     static_assert(W == 256, "keys of 256 threads");
     const int tid = threadIdx.x, shift = k <= 16 ? 3 : k <= 32 ? 2 : 0;
     float g = thread_max;
@@ -725,9 +730,9 @@ __device__ __forceinline__ float refresh_bound(float thread_max, int k, TopShare
         const uint32_t t = shift == 3   ? search_bound<1>(sh.max_key, k)
                            : shift == 2 ? search_bound<2>(sh.max_key, k)
                                         : search_bound<8>(sh.max_key, k);
-        // a thread without an entry above kFloor says about kFloor: no bound then
+        // a thread without an entry above the floor says the floor: no bound then
         const float v = key_value(t);
-        if (tid == 0) sh.bound = v > 0.5f * kFloor ? v : -FLT_MAX;
+        if (tid == 0) sh.bound = v > floor ? v : -FLT_MAX;
     }
     bar<W>();
     return sh.bound;
@@ -777,7 +782,7 @@ __device__ __forceinline__ Sums<true> walk_candidates(const Row<T> &row, const L
     ring_walk<W>(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int) {
         const float mx = s.template add<T, kUnroll>(r, a.c);
         if (++done == next) {
-            bound = refresh_bound<W>(s.m, a.k, sh);
+            bound = refresh_bound<W>(s.m, a.k, floor_of(a.c), sh);
             next = min(4 * next, chunks);
         }
         if (__any_sync(0xffffffffu, mx >= bound)) {
@@ -785,7 +790,7 @@ __device__ __forceinline__ Sums<true> walk_candidates(const Row<T> &row, const L
             for (int u = 0; u < kUnroll; ++u) note<W>(Vec<T>::max(r[u]) >= bound, v + u * W, notes, sh);
         }
     });
-    if (done == 0) bound = refresh_bound<W>(s.m, a.k, sh);  // a row within two vectors
+    if (done == 0) bound = refresh_bound<W>(s.m, a.k, floor_of(a.c), sh);  // a row within two vectors
     note<W>(edge, ve, notes, sh);
     if (notes > kNotes) sh.overflow = 1;
     return s;
@@ -887,7 +892,7 @@ __global__ void __launch_bounds__(W + 32, kCtasPerSm<W>) k_token_logprobs(const 
         if ((threadIdx.x & 31) == 0) buf[turn][threadIdx.x >> 5] = of_warp;
         bar<W>();
         RowSums s = warps_join<W / 32, true>(buf[turn], a.c);
-        if (is_far(s)) {
+        if (is_far(s, a.c)) {
             bar<W>();
             s = far_sums<W>(row, a.c, buf[turn], [](int) { return true; });
         }
@@ -1238,7 +1243,7 @@ __global__ void __launch_bounds__(W + 64, kCtasPerSm<W>) k_distill(const Distill
         RowState st;
         if (!skip) {
             s = warps_join<W / 32, false>(buf[turn], a.c);
-            if (is_far(s)) {
+            if (is_far(s, a.c)) {
                 bar<P>();
                 s = far_sums<P>(row, a.c, buf[turn], [&](int e) {
                     const int at = e + row.mis;
