@@ -313,16 +313,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 // where a 128 x 256 tile of one CTA reads 96, and two thirds of its bytes from L2.
 //
 // Tensor memory has 512 columns: two accumulators of 256 would leave none for the scales.
-// So the accumulators of consecutive tiles start at columns 0 and 160 and overlap in 96;
+// So the accumulators of consecutive tiles start at columns 0 and 96 and overlap in 160;
 // the epilogue drains those first and lets the next tile's MMAs start while it drains the
-// other 160.  The last 96 columns hold the scales of two stages; before a stage's scales
-// are copied, the MMAs of the stage two before it have completed (its ring slot's barrier).
+// other 96.  The last 160 columns hold the scales of three stages (nv) or four (mx): before
+// a stage's scales are copied, the MMAs of the stage that many before it have completed
+// (its ring slot's barrier).  With two, the issuing thread's round trip through that
+// barrier left the tensor pipe idle between stages (48% active; 4096 x 11008 x 4096 nv took
+// 116 us).
 constexpr int kPairThreads = 256;  // producer, issuer, allocator, one idle, four epilogue warps
-constexpr int kAcc1 = 160;         // first column of odd tiles' accumulators
+constexpr int kAcc1 = 96;          // first column of odd tiles' accumulators
 constexpr int kOverlap = 256 - kAcc1;
-constexpr int kScaleCols = 48;     // of one stage: 16 of A, 32 of B
-constexpr int kScaleBase = 512 - 2 * kScaleCols;
-static_assert(kAcc1 + 256 <= kScaleBase && kOverlap % 32 == 0, "tensor memory layout");
+constexpr int kScaleBase = kAcc1 + 256;
+static_assert(kOverlap % 32 == 0, "tensor memory layout");
 
 template <bool NV>
 struct PairCfg {
@@ -331,6 +333,9 @@ struct PairCfg {
     static constexpr int SF_BYTES = SF * kSfTile;  // of 128 rows
     static constexpr int STAGE = 2 * kATile + 3 * SF_BYTES;
     static constexpr int STAGES = 5;
+    static constexpr int SF_COLS = SF * 12;   // scale columns of a stage: a third of A, the rest of B
+    static constexpr int SF_BUFS = NV ? 3 : 4;
+    static_assert(kScaleBase + SF_BUFS * SF_COLS <= 512, "tensor memory columns");
     static constexpr int OUT = 4 * 2 * 2048;  // two 32 x 32 bf16 chunks per epilogue warp
     static constexpr int SMEM = 1024 + STAGES * STAGE + OUT + 256;
     static_assert(STAGE % 1024 == 0 && SMEM <= 232448, "shared memory");
@@ -390,6 +395,29 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void 
                  "r"(smem_u32(smem_src)), "r"(c0), "r"(c1)
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+
+// A stage's scale copies and MMAs (unrolled where the counts are constants).
+template <bool NV>
+__device__ __forceinline__ void issue_stage(uint32_t sa, uint32_t d, uint32_t tsf, int nsf, int nmma, bool accumulate) {
+    using C = PairCfg<NV>;
+    const uint32_t tsfb = tsf + C::SF * 4;
+    const uint64_t sfa = smem_desc_plain(sa + 2 * kATile), sfb = smem_desc_plain(sa + 2 * kATile + C::SF_BYTES);
+#pragma unroll
+    for (int j = 0; j < C::SF; ++j)
+        if (j < nsf) {  // descriptors count 16 bytes
+            tmem_cp_scales_pair(tsf + j * 4, sfa + j * (kSfTile >> 4));
+            tmem_cp_scales_pair(tsfb + j * 8, sfb + j * (kSfTile >> 4));
+            tmem_cp_scales_pair(tsfb + j * 8 + 4, sfb + ((C::SF_BYTES + j * kSfTile) >> 4));
+        }
+    const uint64_t ad = smem_desc_sw128(sa, 16, 1024), bd = smem_desc_sw128(sa + kATile, 16, 1024);
+#pragma unroll
+    for (int kk = 0; kk < kKStage / 64; ++kk)
+        if (kk < nmma) {
+            const int j = NV ? kk : kk >> 1;
+            mma_fp4_pair<NV>(d, ad + 2 * kk, bd + 2 * kk, idesc_fp4_pair(NV, NV ? 0u : (kk & 1) * 2u), tsf + j * 4,
+                             tsfb + j * 8, accumulate || kk > 0 ? 1u : 0u);
+        }
 }
 
 template <bool NV>
@@ -507,8 +535,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                         ok = false;
                         break;
                     }
-                    if (it >= 2) {  // the MMAs that read this scale buffer before
-                        const uint32_t o = it - 2;
+                    if (it >= C::SF_BUFS) {  // the MMAs that read this scale buffer before
+                        const uint32_t o = it - C::SF_BUFS;
                         if (!mbar_wait_bounded(&ctl->empty[o % C::STAGES], (o / C::STAGES) & 1u, abort_flag, p.err,
                                                p.wait_limit_ns)) {
                             ok = false;
@@ -516,24 +544,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                         }
                     }
                     tc_fence_after();
-                    const uint32_t sa = smem_u32(smem + st * C::STAGE), sb = sa + kATile, ssfa = sb + kATile,
-                                   ssfb = ssfa + C::SF_BYTES;
-                    const uint32_t tsf = tmem + kScaleBase + (it & 1u) * kScaleCols, tsfb = tsf + 16;
+                    const uint32_t sa = smem_u32(smem + st * C::STAGE);
+                    const uint32_t tsf = tmem + kScaleBase + (it % C::SF_BUFS) * C::SF_COLS;
                     const int kleft = p.K - kb * kKStage;
-                    const int nsf = kleft >= kKStage ? C::SF : (kleft + C::KSF - 1) / C::KSF;
-                    for (int j = 0; j < nsf; ++j) {
-                        tmem_cp_scales_pair(tsf + j * 4, smem_desc_plain(ssfa + j * kSfTile));
-                        tmem_cp_scales_pair(tsfb + j * 8, smem_desc_plain(ssfb + j * kSfTile));
-                        tmem_cp_scales_pair(tsfb + j * 8 + 4, smem_desc_plain(ssfb + C::SF_BYTES + j * kSfTile));
-                    }
-                    const int nmma = kleft >= kKStage ? kKStage / 64 : (kleft + 63) / 64;
-                    for (int kk = 0; kk < nmma; ++kk) {
-                        const uint64_t ad = smem_desc_sw128(sa + kk * 32, 16, 1024);
-                        const uint64_t bd = smem_desc_sw128(sb + kk * 32, 16, 1024);
-                        const int j = NV ? kk : kk >> 1;
-                        mma_fp4_pair<NV>(d, ad, bd, idesc_fp4_pair(NV, NV ? 0u : (kk & 1) * 2u), tsf + j * 4, tsfb + j * 8,
-                                         (kb > 0 || kk > 0) ? 1u : 0u);
-                    }
+                    if (kleft >= kKStage)
+                        issue_stage<NV>(sa, d, tsf, C::SF, kKStage / 64, kb > 0);
+                    else
+                        issue_stage<NV>(sa, d, tsf, (kleft + C::KSF - 1) / C::KSF, (kleft + 63) / 64, kb > 0);
                     issued = true;
                     tc_commit_pair(&ctl->empty[st], 3);
                 }
