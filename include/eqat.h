@@ -410,7 +410,7 @@ eqat_status eqat_dequant_fp4(const uint8_t *codes, const uint8_t *scales, int64_
                              const float *g, void *values, int dt, eqat_stream_t stream);
 
 /* Bytes of workspace of eqat_fp4_linear_fwd (backward == 0: X's codes and scales; 0 for
- * up to 16 tokens and K <= 32768, whose X is packed inside the product) or
+ * the few tokens, up to 16, whose X is packed inside the product) or
  * eqat_fp4_linear_bwd (the bf16 values of W and X); 0 for bad arguments. */
 size_t eqat_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int backward);
 

@@ -847,7 +847,7 @@ size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 size_t fp4_ws(int64_t M, int64_t N, int64_t K, int fmt, bool backward) {
     const size_t m = static_cast<size_t>(M), n = static_cast<size_t>(N), k = static_cast<size_t>(K);
     if (backward) return up256(n * k * 2) + up256(m * k * 2);
-    if (eqat::fp4_packs_in_product(M, K)) return 0;
+    if (eqat::fp4_packs_in_product(M, N, K)) return 0;
     return up256(m * k / 2) + static_cast<size_t>(fp4_scale_bytes(M, K, fmt));
 }
 
@@ -990,7 +990,7 @@ eqat_status eqat_fp4_linear_fwd(const void *X, const uint8_t *codes, const uint8
         return EQAT_OK;
     }
     const bool nv = fmt == EQAT_FP4_NV;
-    if (eqat::fp4_packs_in_product(M, K)) {
+    if (eqat::fp4_packs_in_product(M, N, K)) {
         EQAT_CUDA(eqat::launch_fp4_few_tokens(X, gx, codes, scales, gw, nv, M, N, K, Y, dev, st), "fp4 product");
         return EQAT_OK;
     }

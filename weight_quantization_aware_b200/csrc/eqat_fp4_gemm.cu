@@ -634,11 +634,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
 // scale tiles itself while the first weights are on their way.  The parts are joined over
 // the cluster's shared memory in the order of the ranks.  The call reads the packed
 // weights once; it is bound by launch and memory latency (the weights of a 4096 x 4096
-// layer are 1.4 us of HBM time).
+// layer are 1.4 us of HBM time, the call takes 5.3), so K is split until the SMs are
+// full, and a part is small enough (2048 values) for two CTAs on an SM.
 constexpr int kDecTokens = 16;
 constexpr int kDecThreads = 256;    // producer, issuer (after packing), packers, of which four drain
-constexpr int kDecMaxSlice = 4096;  // K values of a CTA
-constexpr int kDecStages = 6;
+constexpr int kDecMaxSlice = 2048;  // K values of a CTA
+constexpr int kDecStages = 4;
+constexpr int kDecTmem = 256;       // two CTAs share an SM's 512 columns
+constexpr int kDecSms = 148;
 
 template <bool NV>
 struct DecCfg {
@@ -647,11 +650,29 @@ struct DecCfg {
     static constexpr int STAGE = kATile + 2048;  // A and its scale tiles (mx uses half of that)
     static constexpr int XTILE = kDecTokens * 128;
     static constexpr int XSTAGES = kDecMaxSlice / kKStage;
-    static constexpr int RED = 128 * (kDecTokens + 1) * 4;
-    static constexpr int SMEM = 1024 + kDecStages * STAGE + XSTAGES * (XTILE + SF * kSfTile) + RED + 256;
+    static constexpr int SMEM = 1024 + kDecStages * STAGE + XSTAGES * (XTILE + SF * kSfTile) + 256;
     static constexpr int SF_COLS = SF * 8;
-    static_assert(32 + kDecStages * SF_COLS <= 512 && SMEM <= 232448, "tensor and shared memory");
+    static constexpr int RED = 128 * (kDecTokens + 1) * 4;  // the parts, in the stages' place
+    static_assert(32 + kDecStages * SF_COLS <= kDecTmem && SMEM <= 113 * 1024 && RED <= kDecStages * STAGE,
+                  "two blocks per SM");
 };
+
+// Ranks that split K: enough for the slice that a CTA can pack, then doubled while every
+// SM has one CTA at most (and every rank two stages), or two of at least eight stages.
+// On 11008 x 4096 (86 tiles) two ranks take 7.9 us for one token where one takes 9.9.
+int decode_ranks(int64_t N, int64_t K) {
+    const int64_t tiles = (N + 127) / 128, stages = (K + kKStage - 1) / kKStage;
+    int ranks = 1;
+    while (static_cast<int64_t>(ranks) * kDecMaxSlice < K && ranks < 16) ranks *= 2;
+    while (ranks < 8 && ((2 * ranks * tiles <= kDecSms && stages >= 4 * ranks) ||
+                         (2 * ranks * tiles <= 2 * kDecSms && stages >= 16 * ranks)))
+        ranks *= 2;
+    return ranks;
+}
+int64_t decode_slice(int64_t N, int64_t K) {
+    const int64_t stages = (K + kKStage - 1) / kKStage, ranks = decode_ranks(N, K);
+    return (stages + ranks - 1) / ranks * kKStage;
+}
 
 struct DecArgs {
     const __nv_bfloat16 *X;
@@ -701,14 +722,14 @@ __device__ __forceinline__ void pack_slice(const DecArgs &p, int64_t kbase, int 
 }
 
 template <bool NV>
-__global__ void __launch_bounds__(kDecThreads, 1) k_decode_fp4(const __grid_constant__ CUtensorMap tmW, const DecArgs p) {
+__global__ void __launch_bounds__(kDecThreads, 2) k_decode_fp4(const __grid_constant__ CUtensorMap tmW, const DecArgs p) {
     using C = DecCfg<NV>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     uint8_t *xt = smem + kDecStages * C::STAGE, *xs = xt + C::XSTAGES * C::XTILE;
-    float *red = reinterpret_cast<float *>(xs + C::XSTAGES * C::SF * kSfTile);
-    DecCtl *ctl = reinterpret_cast<DecCtl *>(reinterpret_cast<uint8_t *>(red) + C::RED);
+    DecCtl *ctl = reinterpret_cast<DecCtl *>(xs + C::XSTAGES * C::SF * kSfTile);
+    float *red = reinterpret_cast<float *>(smem);  // once all MMAs have read the stages
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t rank, nranks;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -727,7 +748,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_decode_fp4(const __grid_cons
     pdl_wait();
     if (threadIdx.x == 0) pdl_allow_dependents();
     if (warp == 2) {
-        tmem_alloc(&ctl->tmem_base, 512);
+        tmem_alloc(&ctl->tmem_base, kDecTmem);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -850,7 +871,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) k_decode_fp4(const __grid_cons
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, kDecTmem);
     }
 }
 
@@ -972,12 +993,8 @@ cudaError_t launch_decode(const void *X, const float *gx, const Side &w, int64_t
         if (e != cudaSuccess) return e;
         done.fetch_or(bit);
     }
-    const int64_t tiles = (w.rows + 127) / 128, stages = (K + kKStage - 1) / kKStage;
-    // ranks: enough for the slice that a CTA can pack, then doubled while the SMs last and
-    // every rank keeps two stages
-    int ranks = 1;
-    while (static_cast<int64_t>(ranks) * kDecMaxSlice < K) ranks *= 2;
-    while (ranks < 8 && 2 * ranks * tiles <= dev.sm_count && stages >= 4 * ranks) ranks *= 2;
+    const int64_t tiles = (w.rows + 127) / 128;
+    const int ranks = decode_ranks(w.rows, K);
     if (ranks > 8 || tiles * ranks > 0x7FFFFFFF) return cudaErrorInvalidValue;
     DecArgs p{};
     p.X = static_cast<const __nv_bfloat16 *>(X);
@@ -989,7 +1006,7 @@ cudaError_t launch_decode(const void *X, const float *gx, const Side &w, int64_t
     p.N = w.rows;
     p.K = K;
     p.M = static_cast<int>(M);
-    p.slice = static_cast<int>((stages + ranks - 1) / ranks * kKStage);
+    p.slice = static_cast<int>(decode_slice(w.rows, K));
     p.err = device_error_word();
     if (!p.err) return cudaErrorInvalidSymbol;
     p.wait_limit_ns = kWaitLimitNs;
@@ -1003,7 +1020,12 @@ cudaError_t launch_decode(const void *X, const float *gx, const Side &w, int64_t
 
 }  // namespace
 
-bool fp4_packs_in_product(int64_t M, int64_t K) { return M <= kDecTokens && K <= 8ll * kDecMaxSlice; }
+// The product packs X itself while that is little work for a CTA: 16 tokens by 1024 values
+// or 8 by 2048 (16 by 4096 took 21.5 us on 11008 x 4096, a packing kernel and the plain
+// product 12.0).
+bool fp4_packs_in_product(int64_t M, int64_t N, int64_t K) {
+    return M <= kDecTokens && K <= 8ll * kDecMaxSlice && M * decode_slice(N, K) <= 16 * 1024;
+}
 
 cudaError_t launch_fp4_few_tokens(const void *X, const float *gx, const uint8_t *w_codes, const uint8_t *w_scales,
                                   const float *gw, bool nv, int64_t M, int64_t N, int64_t K, void *Y,

@@ -206,7 +206,7 @@ cudaError_t launch_gemm_fp4(const uint8_t *x_codes, const uint8_t *x_scales, con
                             void *Y, const DeviceInfo &dev, cudaStream_t st);
 
 // Few tokens: X [M, K] bf16 is packed by the product's own kernel (no workspace).
-bool fp4_packs_in_product(int64_t M, int64_t K);
+bool fp4_packs_in_product(int64_t M, int64_t N, int64_t K);
 cudaError_t launch_fp4_few_tokens(const void *X, const float *gx, const uint8_t *w_codes, const uint8_t *w_scales,
                                   const float *gw, bool nv, int64_t M, int64_t N, int64_t K, void *Y,
                                   const DeviceInfo &dev, cudaStream_t st);
