@@ -78,7 +78,9 @@ def check_logprobs(x, targets, k, tau=1.0):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("T,V,k", [(1, 1, 1), (1, 2, 0), (3, 7, 7), (2, 33, 128), (5, 1000, 5), (4, 2049, 128),
-                                   (9, 32000, 1), (3, 50001, 64), (700, 513, 20), (2, 131075, 100), (150, 66001, 0), (20, 70003, 0)])
+                                   (9, 32000, 1), (3, 50001, 64), (700, 513, 20), (2, 131075, 100), (150, 66001, 0), (20, 70003, 0),
+                                   (1300, 301, 32), (1300, 301, 33), (1300, 77, 128), (500, 3001, 7), (500, 8001, 0),
+                                   (2500, 40, 40)])
 def test_logprobs(T, V, k, dtype):
     x = make(T, V, dtype, T * V)
     g = torch.Generator().manual_seed(3)
@@ -178,6 +180,11 @@ def test_top_k_of_uneven_and_tied_rows(dtype):
     x[5, V - 1] = -4.0
     for k in (1, 3, 64, 128):
         check_logprobs(x, torch.arange(6, device="cuda"), k)
+    # the narrow block: short rows, many of them
+    y = x[:, :4001].repeat(90, 1).contiguous()
+    y[::6, 100:] += 0.0
+    for k in (3, 32):
+        check_logprobs(y, torch.arange(len(y), device="cuda"), k)
 
 
 def check_distill(x, ids, tlp, w, tau, tail):
@@ -218,7 +225,8 @@ def teacher(x, k, seed, tau=1.0):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("T,V,k,tau", [(1, 1, 1, 1.0), (2, 5, 5, 1.0), (3, 9, 4, 2.0), (4, 1000, 1, 0.7),
                                        (700, 515, 16, 1.0), (5, 32000, 128, 2.0), (2, 131075, 32, 1.0),
-                                       (150, 66001, 40, 1.0), (20, 70003, 7, 0.5), (2, 300007, 9, 1.0)])
+                                       (150, 66001, 40, 1.0), (20, 70003, 7, 0.5), (2, 300007, 9, 1.0),
+                                       (1300, 301, 32, 1.0), (500, 8001, 128, 2.0), (2500, 40, 40, 1.0)])
 def test_distill(T, V, k, tau, dtype, tail):
     x = make(T, V, dtype, T + V)
     ids, tlp = teacher(x, k, V, tau)

@@ -42,9 +42,13 @@ namespace {
 // rows than SMs.  On 8 rows of 131072 bf16 the wide block takes 17.4 us where the narrow
 // one takes 23.8 (distillation step) and 9.0 against 11.1 (log probabilities); on rows of
 // 32000 they are even (9.4 and 9.6, 5.2 and 4.5), on shorter ones the narrow one wins.
-// With alternatives the narrow block does: its bound has fewer maxima to rank (22.7
-// against 17.3 us on those rows).
-constexpr int kWalk = 256, kWalkWide = 768;
+// With alternatives the block of 256 does: its bound has fewer maxima to rank (22.7
+// against 17.3 us on those rows).  64 threads, eight to twelve blocks per SM, walk many
+// short rows: what a row costs besides its walk (joins, slots, alternatives) then runs
+// for more rows at a time.  4096 rows of 1000 bf16 take 8.1 us (log probabilities) and 20.9
+// (distillation step) where blocks of 256 take 20.7 and 49.5; 4096 of 16000 take 28.8 and
+// 80.3 against 33.0 and 85.3, and 4096 of 32000 are slower (53.9, 143 against 53.4, 127).
+constexpr int kWalkNarrow = 64, kWalk = 256, kWalkWide = 768;
 constexpr int kUnroll = 4;  // 16-byte vectors per thread and chunk
 constexpr int kStages = 3;  // chunks of the ring
 template <int W>
@@ -52,10 +56,11 @@ constexpr int kChunk = W * kUnroll;  // vectors of a chunk: 16 KB, or 48 KB
 template <int W>
 constexpr size_t kRingBytes = static_cast<size_t>(kStages) * kChunk<W> * 16;
 template <int W>
-constexpr int kCtasPerSm = W == kWalk ? 3 : 1;
+constexpr int kCtasPerSm = W == kWalkNarrow ? 8 : W == kWalk ? 3 : 1;
 constexpr uint64_t kWaitLimitNs = 4000000000ull;     // far above any legitimate wait
 constexpr int kNotes = 256;        // vectors that a warp notes for the top-k selection, in shared memory
 constexpr int kKept = 1024;        // entries among them that are ranked
+constexpr int64_t kNarrowBytes = 32 * 1024;  // of a row, at most, for the narrow block
 constexpr size_t kWideBitBytes = 64 * 1024;  // bitmaps beside the wide ring: V up to 262000
 constexpr uint32_t kNegInfBf16x2 = 0xFF80FF80u;
 constexpr uint32_t kNegInfF32 = 0xFF800000u;
@@ -605,7 +610,7 @@ __device__ __forceinline__ bool is_far(const RowSums &s, float c) { return s.m <
 
 // Blocks per SM of the log probabilities' kernels: see launch_logprobs_t.
 template <bool TOP, int W>
-constexpr int kLogprobCtas = W != kWalk ? 1 : TOP ? 3 : 4;
+constexpr int kLogprobCtas = W == kWalkNarrow ? (TOP ? 8 : 12) : W == kWalkWide ? 1 : TOP ? 3 : 4;
 
 struct LogprobArgs {
     const void *x;
@@ -719,21 +724,28 @@ __device__ __forceinline__ uint32_t search_bound(const uint32_t *keys, int k) {
 }
 
 // A value that at least k entries walked so far reach (-FLT_MAX while there are fewer):
-// the k-th largest of the maxima of the threads, or for small k of groups of 4 or 8 of
-// them (still at least 2 k; for k = 64 pairs gave more candidates than they saved), found
-// by one warp.
+// the k-th largest of the maxima of the threads, or for small k of groups of 2, 4 or 8 of
+// them (at least 4 k groups: with 2 k, k = 64 gave more candidates than they saved),
+// found by one warp.  `live`: threads that have entries.
 template <int W>
-__device__ __forceinline__ float refresh_bound(float thread_max, int k, float floor, TopShared<W> &sh) {
-    static_assert(W == 256, "keys of 256 threads");
-    const int tid = threadIdx.x, shift = k <= 16 ? 3 : k <= 32 ? 2 : 0;
+__device__ __forceinline__ float refresh_bound(float thread_max, int k, int live, float floor, TopShared<W> &sh) {
+    static_assert(W == 64 || W == 256, "32 Q keys");
+    const int tid = threadIdx.x;
+    int shift = 0;
+    while (((min(live, W) >> (shift + 1)) >= 4 * k) && (W >> (shift + 1)) >= 32) ++shift;
     float g = thread_max;
     for (int i = 0; i < shift; ++i) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1 << i));
     if ((tid & ((1 << shift) - 1)) == 0) sh.max_key[tid >> shift] = order_key(g);
     bar<W>();
     if (tid < 32) {
-        const uint32_t t = shift == 3   ? search_bound<1>(sh.max_key, k)
-                           : shift == 2 ? search_bound<2>(sh.max_key, k)
-                                        : search_bound<8>(sh.max_key, k);
+        const int keys = W >> shift;
+        uint32_t t;
+        if (W == 256 && keys == 256)
+            t = search_bound<8>(sh.max_key, k);
+        else if (W == 256 && keys == 128)
+            t = search_bound<4>(sh.max_key, k);
+        else
+            t = keys == 64 ? search_bound<2>(sh.max_key, k) : search_bound<1>(sh.max_key, k);
         // a thread without an entry above the floor says the floor: no bound then
         const float v = key_value(t);
         if (tid == 0) sh.bound = v > floor ? v : -FLT_MAX;
@@ -786,7 +798,7 @@ __device__ __forceinline__ Sums<true> walk_candidates(const Row<T> &row, const L
     ring_walk<W>(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int) {
         const float mx = s.template add<T, kUnroll>(r, a.c);
         if (++done == next) {
-            bound = refresh_bound<W>(s.m, a.k, floor_of(a.c), sh);
+            bound = refresh_bound<W>(s.m, a.k, row.b1 - row.b0, floor_of(a.c), sh);
             next = min(4 * next, chunks);
         }
         if (__any_sync(0xffffffffu, mx >= bound)) {
@@ -794,7 +806,7 @@ __device__ __forceinline__ Sums<true> walk_candidates(const Row<T> &row, const L
             for (int u = 0; u < kUnroll; ++u) note<W>(Vec<T>::max(r[u]) >= bound, v + u * W, notes, sh);
         }
     });
-    if (done == 0) bound = refresh_bound<W>(s.m, a.k, floor_of(a.c), sh);  // a row within two vectors
+    if (done == 0) bound = refresh_bound<W>(s.m, a.k, row.b1 - row.b0, floor_of(a.c), sh);  // a row within two vectors
     note<W>(edge, ve, notes, sh);
     if (notes > kNotes) sh.overflow = 1;
     return s;
@@ -1334,11 +1346,24 @@ inline bool few_long_rows(int64_t T, int64_t row_bytes, const DeviceInfo &dev) {
     return T <= dev.sm_count && row_bytes >= 128 * 1024;
 }
 
+// Rows for the narrow block: short ones beyond the SMs, longer ones beyond the blocks of
+// kWalk (see kWalkNarrow).
+inline bool many_short_rows(int64_t T, int64_t row_bytes, const DeviceInfo &dev) {
+    return row_bytes <= kNarrowBytes && T > (row_bytes <= 8 * 1024 ? 1 : 3) * static_cast<int64_t>(dev.sm_count);
+}
+
 template <typename T>
 cudaError_t launch_logprobs_t(const LogprobArgs &a, const DeviceInfo &dev, cudaStream_t st) {
     const int64_t row_bytes = a.V * static_cast<int64_t>(sizeof(T));
-    if (a.k > 0) return launch_logprobs_w<T, true, kWalk>(a, kLogprobCtas<true, kWalk>, dev, st);
+    const bool narrow = many_short_rows(a.T, row_bytes, dev);
+    if (a.k > 0) {
+        // the narrow block has 64 maxima to take a bound from
+        return narrow && a.k <= 32 ? launch_logprobs_w<T, true, kWalkNarrow>(a, kLogprobCtas<true, kWalkNarrow>, dev, st)
+                                   : launch_logprobs_w<T, true, kWalk>(a, kLogprobCtas<true, kWalk>, dev, st);
+    }
     if (few_long_rows(a.T, row_bytes, dev)) return launch_logprobs_w<T, false, kWalkWide>(a, 1, dev, st);
+    if (narrow)
+        return launch_logprobs_w<T, false, kWalkNarrow>(a, kLogprobCtas<false, kWalkNarrow>, dev, st);
     // Four blocks per SM on short rows (2048 x 32000 bf16: 29.6 us against 32.2 with three),
     // three on long ones (1024 x 131072: 49.9 against 52.6).
     return launch_logprobs_w<T, false, kWalk>(a, row_bytes <= 96 * 1024 ? 4 : 3, dev, st);
@@ -1350,7 +1375,9 @@ cudaError_t launch_distill_w(const DistillArgs &a, const DeviceInfo &dev, cudaSt
     auto kern = k_distill<T, TAIL, W>;
     // two bits per vocabulary entry: the wide block's ring leaves room for fewer entries
     const size_t bits = static_cast<size_t>((a.V + Vec<T>::N + 31) / 32) * 8;
-    constexpr size_t most = W == kWalk ? static_cast<size_t>((kDistillMaxV + 64) / 4) : kWideBitBytes;
+    constexpr size_t most = W == kWalk       ? static_cast<size_t>((kDistillMaxV + 64) / 4)
+                            : W == kWalkWide ? kWideBitBytes
+                                             : static_cast<size_t>(kNarrowBytes);
     cudaError_t e = allow_smem(kern, kRingBytes<W> + most, done, dev);
     if (e != cudaSuccess) return e;
     // The rows that are walked twice at a time have to stay in the 126 MB L2 beside what
@@ -1366,7 +1393,9 @@ cudaError_t launch_distill_w(const DistillArgs &a, const DeviceInfo &dev, cudaSt
 template <typename T, bool TAIL>
 cudaError_t launch_distill_t(const DistillArgs &a, const DeviceInfo &dev, cudaStream_t st) {
     const size_t bits = static_cast<size_t>((a.V + Vec<T>::N + 31) / 32) * 8;
-    const bool wide = few_long_rows(a.T, a.V * static_cast<int64_t>(sizeof(T)), dev) && bits <= kWideBitBytes;
+    const int64_t row_bytes = a.V * static_cast<int64_t>(sizeof(T));
+    if (many_short_rows(a.T, row_bytes, dev)) return launch_distill_w<T, TAIL, kWalkNarrow>(a, dev, st);
+    const bool wide = few_long_rows(a.T, row_bytes, dev) && bits <= kWideBitBytes;
     return wide ? launch_distill_w<T, TAIL, kWalkWide>(a, dev, st) : launch_distill_w<T, TAIL, kWalk>(a, dev, st);
 }
 
