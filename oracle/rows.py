@@ -72,7 +72,7 @@ def distill_topk(x, ids, tlp, weight=None, temperature=1.0, tail=False):
         p = np.exp(logp)
         m = q > 0
         L = (q[m] * (lq[m] - logp[slots[m]])).sum()
-        factor = np.ones(V)
+        g = p.copy()
         if tail:
             outside = np.ones(V, bool)
             outside[slots] = False
@@ -80,8 +80,7 @@ def distill_topk(x, ids, tlp, weight=None, temperature=1.0, tail=False):
             lpr = _lse(z[outside]) - lse if outside.any() else -np.inf
             if qr > 0 and lpr > -np.inf:
                 L += qr * (np.log(qr) - lpr)
-                factor[outside] -= qr * np.exp(-lpr)
-        g = p * factor
+                g[outside] -= qr * np.exp(logp[outside] - lpr)
         np.subtract.at(g, slots, q)
         loss[t] = w * L
         grad[t] = g * (w / temperature)

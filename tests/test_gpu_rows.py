@@ -87,6 +87,24 @@ def test_logprobs(T, V, k, dtype):
     check_logprobs(x, torch.randint(0, V, (T,), generator=g).cuda(), min(k, 128))
 
 
+def test_logits_beyond_two_to_the_31():
+    """m c = RN(m c) + up to 128: 2^-y and 2^y of that leave fp32 on either side.  Entries
+    are at least 128 apart there, so that a row's probability is that of its largest."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    x = 1.5e9 + 1.4e9 * torch.rand(3000, 64, generator=gen, device="cuda")
+    x[1::2] *= -1
+    check_logprobs(x, x.argmax(1), 3)
+    check_logprobs(x, torch.arange(3000, device="cuda") % 64, 0)
+    ids = torch.arange(6, device="cuda").repeat(3000, 1)
+    tlp = torch.log_softmax(torch.randn(3000, 7, generator=gen, device="cuda"), 1)[:, :6].contiguous()
+    for tail in (False, True):
+        want_l, want_g = orc.distill_topk(f64(x), ids.cpu().numpy(), f64(tlp), None, 1.0, tail)
+        loss, grad = eqat.distill_topk_step(x, ids, tlp, tail=tail)
+        # q_i within 2^-21 of itself, z - lse within 2^-53 of z, the loss rounded once
+        assert np.abs(f64(loss) - want_l).max() <= 2.0 ** -20 * np.abs(want_l).max()
+        assert np.abs(f64(grad) - want_g).max() <= 2.0 ** -20
+
+
 @pytest.mark.parametrize("tau", [0.25, 3.0, 1e-6, 1e6])
 def test_logprobs_temperature(tau):
     x = make(6, 4097, torch.float32, 1)

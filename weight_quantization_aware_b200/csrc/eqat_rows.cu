@@ -7,11 +7,11 @@
 // maximum m, S = sum 2^y and (for the entropy) A = sum 2^y y per thread, with
 // y = (x - m) c and c = log2(e) / temperature.  y is one fma, x c - RN(m c), and what
 // the rounding of m c moved all of a thread's terms by is taken out of S and A at the
-// end (m c - RN(m c) is exact in one fma).  That form needs |m c| well below 2^31, where
-// RN would move it by more than ex2 can say: m starts from a floor of -2^23 / c, which
+// end (m c - RN(m c) is exact in one fma).  That form needs |m c| below 2^30, from where
+// RN moves it by more than ex2 can say: m starts from a floor of -2^23 / c, which
 // also keeps masked entries of any kind (-inf, the type's lowest value, -1e10) from being
-// a reference.  A row without an entry above the floor, or whose S is not finite (a NaN,
-// an infinity, values beyond 2^31 / c), is walked again with x - m formed first.  The
+// a reference.  A row without an entry above the floor, with one of 2^30 / c or more, or
+// whose S is not finite (a NaN, an infinity) is walked again with x - m formed first.  The
 // second walk (top alternatives, gradient) reads the row again while it is in L2.
 //
 // What bounds the first walk besides memory is ex2 (a quarter of the issue rate), then
@@ -52,7 +52,7 @@ constexpr int kWalkNarrow = 64, kWalk = 256, kWalkWide = 768;
 constexpr int kUnroll = 4;  // 16-byte vectors per thread and chunk
 constexpr int kStages = 3;  // chunks of the ring
 template <int W>
-constexpr int kChunk = W * kUnroll;  // vectors of a chunk: 16 KB, or 48 KB
+constexpr int kChunk = W * kUnroll;  // vectors of a chunk: 4, 16 or 48 KB
 template <int W>
 constexpr size_t kRingBytes = static_cast<size_t>(kStages) * kChunk<W> * 16;
 template <int W>
@@ -603,8 +603,11 @@ __device__ __noinline__ RowSums far_sums(const Row<T> row, float c, RowSums *buf
     return r;
 }
 
-// No entry above the floor, or no finite sum.
-__device__ __forceinline__ bool is_far(const RowSums &s, float c) { return s.m <= floor_of(c) || !(s.S < INFINITY); }
+// No entry above the floor, no finite sum, or a maximum whose m c is rounded by so much
+// (32 from 2^30 on) that 2^y of the rounding, and y times it, near the ends of fp32.
+__device__ __forceinline__ bool is_far(const RowSums &s, float c) {
+    return s.m <= floor_of(c) || !(s.S < INFINITY) || s.m * c >= 0x1p30f;
+}
 
 // ------------------------------------------------------------------ log probabilities
 
