@@ -57,3 +57,21 @@ def test_head_step(orc, T, tail):
     sure = np.abs(ds_ref) > 0.05 * np.abs(ds_ref).max()
     assert np.array_equal(np.sign(moved)[sure], np.sign(p_ref - sn)[sure])
     assert np.abs(moved).max() <= 2.1e-5
+
+
+def test_head_steps_of_many_then_few_tokens():
+    """The head's workspace follows the token count: a narrow layer needs more for few
+    tokens (partial sums) than for many (W-hat)."""
+    V, K, bits, g = 8, 128, 2, 64
+    d = synthetic.draw_linear(np.random.default_rng(8), 40, V, K, 0.1, "bf16")
+    X, W = d["X"].cuda(), d["W"].cuda()
+    s, z = eqat.minmax_init(W, bits, g)
+    codes, zq = eqat.pack_codes(W, s, z, bits, g)
+    ids, tlp = e2eqp.teacher_alternatives((X.float() @ W.float().t()).to(torch.bfloat16), 4)
+    cfg = e2eqp.E2EQPConfig(bits=bits, group=g)
+    head = e2eqp.QuantHead(codes, zq, s.clone())
+    for step, T in enumerate((40, 8, 3, 40), 1):
+        alone = e2eqp.QuantHead(codes, zq, head.s.clone())
+        want, want_dx = e2eqp.e2eqp_head_step(alone, X[:T], ids[:T], tlp[:T], cfg, 1)
+        loss, dX = e2eqp.e2eqp_head_step(head, X[:T], ids[:T], tlp[:T], cfg, step)
+        assert torch.equal(loss, want) and torch.equal(dX, want_dx)

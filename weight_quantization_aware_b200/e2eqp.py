@@ -21,7 +21,8 @@ from dataclasses import dataclass
 
 import torch
 
-from . import adamw_step, cosine_lr, distill_topk_step, dq_linear_bwd_s, dq_linear_fwd, token_logprobs, workspace
+from . import (EQAT_BF16, adamw_step, cosine_lr, distill_topk_step, dq_linear_bwd_s, dq_linear_fwd, load_library,
+               token_logprobs, workspace)
 
 
 @dataclass
@@ -61,7 +62,8 @@ def e2eqp_head_step(head: QuantHead, X, ids, tlp, cfg: E2EQPConfig, step: int, w
     (default: 1 / T each, the mean over the tokens)."""
     T, K = X.shape
     N = head.codes.shape[0]
-    if head.ws is None or head.ws.numel() < N * K * 2:
+    need = load_library().eqat_workspace_bytes(T, N, K, cfg.bits, cfg.group, EQAT_BF16)
+    if head.ws is None or head.ws.numel() < need:  # few tokens of a narrow layer need more than many
         head.ws = workspace(T, N, K, cfg.bits, cfg.group, X.dtype, X.device)
     if weight is None:
         weight = torch.full((T,), 1.0 / T, dtype=torch.float32, device=X.device)
