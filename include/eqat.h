@@ -401,7 +401,7 @@ eqat_status eqat_pack_fp4(const void *x, int dt, int64_t N, int64_t K, int fmt, 
                           uint8_t *scales, eqat_stream_t stream);
 
 /* The values that packing would store, x_hat [N, K] of dtype dt (exact in bf16 when g
- * is a power of two; otherwise rounded to nearest even). */
+ * is a power of two; otherwise rounded to nearest even).  x_hat may be x itself. */
 eqat_status eqat_fake_quant_fp4(const void *x, int dt, int64_t N, int64_t K, int fmt, const float *g, void *x_hat,
                                 eqat_stream_t stream);
 

@@ -84,6 +84,28 @@ def test_pack_matches_the_oracle(shape, dtype, fmt):
     check_pack(edge_values(*shape, dtype, 1), fmt, None if fmt == "mx" else 2.0 ** -4)
 
 
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_fake_quant_in_place(fmt):
+    for dtype in (torch.bfloat16, torch.float32):
+        W = draw(1500, 2080, dtype, 4).cuda()
+        want = eqat.fake_quant_fp4(W, fmt)
+        assert eqat.fake_quant_fp4(W, fmt, W_hat=W) is W and torch.equal(W, want)
+
+
+@pytest.mark.parametrize("M", [2, 40, 150])
+def test_largest_tensor_scales(M):
+    """Tensor scales whose product is beyond fp32: a sum of 0 stays 0."""
+    g = torch.full((1,), 2.0 ** 100, device="cuda")
+    X, W = torch.zeros(M, 256, dtype=torch.bfloat16, device="cuda"), torch.zeros(136, 256, dtype=torch.bfloat16, device="cuda")
+    X[:, :16], W[:, 16:32] = 2.0 ** 100, 2.0 ** 100
+    X[0, 40], W[3, 40] = 2.0 ** 100, -2.0 ** 100
+    codes, scales = eqat.pack_fp4(W, "nv", tscale=g)
+    Y = f32(eqat.fp4_linear_fwd(X, codes, scales, "nv", tscale=g, x_tscale=g))
+    want = np.zeros((M, 136), np.float32)
+    want[0, 3] = -np.inf
+    assert np.array_equal(Y, want)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 def test_any_tensor_scale(dtype):
     """A tensor scale that is not a power of two: the same fp32 operations in the same order."""

@@ -690,7 +690,7 @@ def pack_fp4(W, fmt, tscale=None, codes=None, scales=None):
 
 
 def fake_quant_fp4(W, fmt, tscale=None, W_hat=None):
-    """The values that pack_fp4 would store, in W's dtype."""
+    """The values that pack_fp4 would store, in W's dtype (W_hat may be W itself)."""
     f = _fmt(fmt)
     lib, dev, stream = _enter()
     N, K = _fp4_matrix(W)

@@ -2,11 +2,12 @@
 // K-major e2m1 codes, a scale for each block of 16 (e4m3) or 32 (e8m0) of K on both
 // sides, fp32 accumulation in tensor memory (tcgen05.mma, block-scaled kinds).
 //
-// Y[M, N] = X W^T runs with the tokens as the 128 rows of a tile, or, for few tokens,
-// with the weights as the rows (SWAP): the tile is then as narrow as the tokens, and the
-// call streams the weights once.
+// Y[M, N] = X W^T takes one of three kernels: up to 16 tokens a cluster per 128 weight rows
+// (k_decode_fp4), up to 128 tokens a CTA per 128 weight rows (k_gemm_fp4: the tile is as
+// narrow as the tokens, and the call streams the weights once), and beyond that CTA pairs
+// (k_gemm2_fp4), whose 256 x 256 tiles reuse what they read.
 //
-// A CTA makes one 128 x NT tile.  A producer thread brings stages of 256 K values: the
+// k_gemm_fp4: a CTA makes one 128 x NT tile of W X^T.  A producer thread brings stages of 256 K values: the
 // code tiles by TMA (128 bytes of K per row, 128-byte swizzle) and the scale tiles by
 // bulk copies.  The issuing thread copies a stage's scale tiles from shared to tensor
 // memory (tcgen05.cp, ordered before the MMAs that read them) and issues one MMA per 64
@@ -38,13 +39,13 @@ template <int NT, bool NV>
 struct Cfg {
     static constexpr int SF = NV ? 4 : 2;              // scale tiles of a stage per 128 rows
     static constexpr int KSF = NV ? 64 : 128;          // K values of a scale tile
-    static constexpr int RB = NT > 128 ? 2 : 1;        // 128-row scale tiles of B
     static constexpr int BTILE = NT * 128;
-    static constexpr int STAGE = kATile + BTILE + SF * kSfTile * (1 + RB);
-    static constexpr int STAGES = NT >= 256 ? 4 : NT >= 128 ? 6 : NT >= 64 ? 7 : 8;
+    static constexpr int STAGE = kATile + BTILE + 2 * SF * kSfTile;
+    static constexpr int STAGES = NT >= 128 ? 6 : NT >= 64 ? 7 : 8;
     static constexpr int SMEM = 1024 + STAGES * STAGE + 256;
     static constexpr int ACC = NT < 32 ? 32 : NT;      // accumulator columns
-    static constexpr int SF_COLS = SF * 4 * (1 + RB);  // scale columns of a stage
+    static constexpr int SF_COLS = 2 * SF * 4;         // scale columns of a stage
+    static_assert(NT <= 128, "one scale tile covers the rows of B");
     static_assert(ACC + STAGES * SF_COLS <= 512, "tensor memory columns");
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(STAGE % 1024 == 0, "swizzled tiles start on 1024 bytes");
@@ -63,9 +64,7 @@ struct Args {
     int64_t rows_a, rows_b;     // rows of A and B
     int K;
     const float *ga, *gb;       // tensor scales (nullable)
-    __nv_bfloat16 *Y;
-    int64_t ldy;
-    int tiles_a;
+    __nv_bfloat16 *Y;           // [rows_b, rows_a]
     int *err;
     uint64_t wait_limit_ns;
 };
@@ -141,7 +140,11 @@ __device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-template <int NT, bool NV, bool SWAP>
+// A sum and its tensor scales, one after the other: their product alone may be infinite
+// (2^100 each) where the sum is 0.
+__device__ __forceinline__ float scaled(float sum, float ga, float gb) { return __fmul_rn(__fmul_rn(sum, ga), gb); }
+
+template <int NT, bool NV>
 __global__ void __launch_bounds__(kThreads, 1)
     k_gemm_fp4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Args p) {
     using C = Cfg<NT, NV>;
@@ -173,16 +176,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
     volatile int *abort_flag = &ctl->abort_flag;
-    const int ta = blockIdx.x % p.tiles_a, tb = blockIdx.x / p.tiles_a;
+    const int ta = blockIdx.x;
     const int nkb = (p.K + kKStage - 1) / kKStage;
 
     if (warp == 0) {
         if (elect_one_sync()) {
             uint32_t armed = 0, armed_parity = 0;
             bool ok = true;
-            // scale tiles of B that exist (its rows past the last tile of 128 have none)
-            const int rb = C::RB == 1 || static_cast<int64_t>(tb) * NT + 128 < p.rows_b ? C::RB : 1;
-            const int64_t b_rowtile = static_cast<int64_t>(tb) * NT / 128;
             for (int kb = 0; kb < nkb; ++kb) {
                 const int st = kb % C::STAGES;
                 const uint32_t ph = (kb / C::STAGES) & 1u;
@@ -195,15 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t sf0 = static_cast<int64_t>(kb) * C::SF;
                 const int64_t left = p.sf_tiles_k - sf0;
                 const uint32_t sf_bytes = static_cast<uint32_t>(left < C::SF ? left : C::SF) * kSfTile;
-                mbar_arrive_expect_tx(&ctl->full[st], kATile + C::BTILE + sf_bytes * (1 + rb));
+                mbar_arrive_expect_tx(&ctl->full[st], kATile + C::BTILE + 2 * sf_bytes);
                 armed |= 1u << st;
                 armed_parity = (armed_parity & ~(1u << st)) | (ph << st);
                 tma_load_2d(sa, &tmA, &ctl->full[st], kb * 128, ta * 128);
-                tma_load_2d(sb, &tmB, &ctl->full[st], kb * 128, tb * NT);
+                tma_load_2d(sb, &tmB, &ctl->full[st], kb * 128, 0);
                 bulk_load(sfa, p.sfa + (ta * p.sf_tiles_k + sf0) * kSfTile, sf_bytes, &ctl->full[st]);
-                for (int h = 0; h < rb; ++h)
-                    bulk_load(sfb + h * C::SF * kSfTile, p.sfb + ((b_rowtile + h) * p.sf_tiles_k + sf0) * kSfTile,
-                              sf_bytes, &ctl->full[st]);
+                bulk_load(sfb, p.sfb + sf0 * kSfTile, sf_bytes, &ctl->full[st]);
             }
             if (!ok) {  // let the copies already issued land before the block exits
                 for (int st = 0; st < C::STAGES; ++st)
@@ -235,10 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int nsf = kleft >= kKStage ? C::SF : (kleft + C::KSF - 1) / C::KSF;
                 for (int j = 0; j < nsf; ++j) {
                     tmem_cp_scales(tsf + j * 4, smem_desc_plain(ssfa + j * kSfTile));
-#pragma unroll
-                    for (int h = 0; h < C::RB; ++h)
-                        tmem_cp_scales(tsf + C::SF * 4 + (j * C::RB + h) * 4,
-                                       smem_desc_plain(ssfb + (h * C::SF + j) * kSfTile));
+                    tmem_cp_scales(tsf + C::SF * 4 + j * 4, smem_desc_plain(ssfb + j * kSfTile));
                 }
                 const int nmma = kleft >= kKStage ? kKStage / 64 : (kleft + 63) / 64;
                 for (int kk = 0; kk < nmma; ++kk) {
@@ -246,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t bd = smem_desc_sw128(sb + kk * 32, 16, 1024);
                     const int j = NV ? kk : kk >> 1;
                     const uint32_t id = NV ? 0u : (kk & 1) * 2u;
-                    mma_fp4<NV>(tmem, ad, bd, idesc_fp4(NT, NV, id), tsf + j * 4, tsf + C::SF * 4 + j * C::RB * 4,
+                    mma_fp4<NV>(tmem, ad, bd, idesc_fp4(NT, NV, id), tsf + j * 4, tsf + C::SF * 4 + j * 4,
                                 (kb > 0 || kk > 0) ? 1u : 0u);
                 }
                 tc_commit(&ctl->empty[st]);
@@ -264,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         const int quad = warp & 3;
-        const float alpha = (p.ga ? __ldg(p.ga) : 1.0f) * (p.gb ? __ldg(p.gb) : 1.0f);
+        const float ga = p.ga ? __ldg(p.ga) : 1.0f, gb = p.gb ? __ldg(p.gb) : 1.0f;
         const bool ok = mbar_wait_bounded(&ctl->acc_full, 0, abort_flag, p.err, p.wait_limit_ns);
         if (__all_sync(0xffffffffu, ok)) {
             tc_fence_after();
@@ -274,26 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c0 = 0; c0 < NT; c0 += 16) {
                 float v[16];
                 tmem_ld_16cols(taddr + c0, v);
-                const int64_t col = static_cast<int64_t>(tb) * NT + c0;
                 if (row >= p.rows_a) continue;
-                if (SWAP) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (col + j < p.rows_b)
-                            p.Y[(col + j) * p.ldy + row] = __float2bfloat16_rn(__fmul_rn(v[j], alpha));
-                } else {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)  // rows of Y are multiples of 8 values
-                        if (col + 8 * q < p.rows_b) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                w[j] = pack_bf16x2(__fmul_rn(v[8 * q + 2 * j], alpha),
-                                                   __fmul_rn(v[8 * q + 2 * j + 1], alpha));
-                            *reinterpret_cast<uint4 *>(p.Y + row * p.ldy + col + 8 * q) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                }
+                for (int j = 0; j < 16; ++j)  // a warp's 32 rows are 32 neighbours of a row of Y
+                    if (c0 + j < p.rows_b) p.Y[(c0 + j) * p.rows_a + row] = __float2bfloat16_rn(scaled(v[j], ga, gb));
             }
         }
     }
@@ -569,7 +548,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         // ---------------------------------------------------------- epilogue (both CTAs)
         const int quad = warp & 3;
         uint8_t *buf = out + quad * 4096;
-        const float alpha = (p.ga ? __ldg(p.ga) : 1.0f) * (p.gb ? __ldg(p.gb) : 1.0f);
+        const float ga = p.ga ? __ldg(p.ga) : 1.0f, gb = p.gb ? __ldg(p.gb) : 1.0f;
         uint32_t local = 0, chunk = 0;
         for (int t = pair; t < p.tiles; t += npairs, ++local) {
             const bool ok = mbar_wait_bounded(&ctl->acc_full, local & 1u, abort_flag, p.err, p.wait_limit_ns);
@@ -589,7 +568,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                     uint32_t w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        w[j] = pack_bf16x2(__fmul_rn(v[8 * q + 2 * j], alpha), __fmul_rn(v[8 * q + 2 * j + 1], alpha));
+                        w[j] = pack_bf16x2(scaled(v[8 * q + 2 * j], ga, gb), scaled(v[8 * q + 2 * j + 1], ga, gb));
                     *reinterpret_cast<uint4 *>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
                         make_uint4(w[0], w[1], w[2], w[3]);
                 }
@@ -852,7 +831,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_decode_fp4(const __grid_cons
     tc_fence_before();
     // the parts are complete in every CTA of the cluster
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    const float alpha = (p.gx ? __ldg(p.gx) : 1.0f) * (p.gw ? __ldg(p.gw) : 1.0f);
+    const float gx = p.gx ? __ldg(p.gx) : 1.0f, gw = p.gw ? __ldg(p.gw) : 1.0f;
     const int rows = 128 / static_cast<int>(nranks);  // of this rank
     for (int i = threadIdx.x; i < rows * p.M; i += kDecThreads) {
         const int row = static_cast<int>(rank) * rows + i % rows, m = i / rows;
@@ -865,7 +844,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_decode_fp4(const __grid_cons
                          : "r"(map_to_rank(&red[row * (kDecTokens + 1) + m], q)));
             sum = __fadd_rn(sum, part);
         }
-        if (n < p.N) p.Y[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(__fmul_rn(sum, alpha));
+        if (n < p.N) p.Y[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(scaled(sum, gx, gw));
     }
     // no CTA leaves while another may read its part
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -881,9 +860,8 @@ struct Side {
     int64_t rows;
 };
 
-template <int NT, bool NV, bool SWAP>
-cudaError_t launch_t(const Side &a, const Side &b, int64_t K, void *Y, int64_t ldy, const DeviceInfo &dev,
-                     cudaStream_t st) {
+template <int NT, bool NV>
+cudaError_t launch_t(const Side &a, const Side &b, int64_t K, void *Y, const DeviceInfo &dev, cudaStream_t st) {
     using C = Cfg<NT, NV>;
     CUtensorMap ma, mb;
     cudaError_t e = encode_map_2d(ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, K / 2, a.rows, K / 2, 128, 128,
@@ -892,7 +870,7 @@ cudaError_t launch_t(const Side &a, const Side &b, int64_t K, void *Y, int64_t l
     e = encode_map_2d(mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, b.codes, K / 2, b.rows, K / 2, 128, NT,
                       CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    auto kern = k_gemm_fp4<NT, NV, SWAP>;
+    auto kern = k_gemm_fp4<NT, NV>;
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (dev.device & 63);
     if (!(done.load() & bit)) {
@@ -910,13 +888,10 @@ cudaError_t launch_t(const Side &a, const Side &b, int64_t K, void *Y, int64_t l
     p.ga = a.g;
     p.gb = b.g;
     p.Y = static_cast<__nv_bfloat16 *>(Y);
-    p.ldy = ldy;
-    p.tiles_a = static_cast<int>((a.rows + 127) / 128);
     p.err = device_error_word();
     if (!p.err) return cudaErrorInvalidSymbol;
     p.wait_limit_ns = kWaitLimitNs;
-    const int64_t tiles = static_cast<int64_t>(p.tiles_a) * ((b.rows + NT - 1) / NT);
-    if (tiles > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    const int64_t tiles = (a.rows + 127) / 128;  // rows are below 2^31
     return launch_pdl(kern, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), C::SMEM, st, ma, mb, p);
 }
 
@@ -969,11 +944,11 @@ cudaError_t launch_pair(const Side &a, const Side &b, int64_t K, void *Y, const 
 
 template <bool NV>
 cudaError_t dispatch(const Side &x, const Side &w, int64_t K, void *Y, const DeviceInfo &dev, cudaStream_t st) {
-    const int64_t M = x.rows, N = w.rows;
-    if (M <= 16) return launch_t<16, NV, true>(w, x, K, Y, N, dev, st);
-    if (M <= 32) return launch_t<32, NV, true>(w, x, K, Y, N, dev, st);
-    if (M <= 64) return launch_t<64, NV, true>(w, x, K, Y, N, dev, st);
-    if (M <= 128) return launch_t<128, NV, true>(w, x, K, Y, N, dev, st);
+    const int64_t M = x.rows;
+    if (M <= 16) return launch_t<16, NV>(w, x, K, Y, dev, st);
+    if (M <= 32) return launch_t<32, NV>(w, x, K, Y, dev, st);
+    if (M <= 64) return launch_t<64, NV>(w, x, K, Y, dev, st);
+    if (M <= 128) return launch_t<128, NV>(w, x, K, Y, dev, st);
     return launch_pair<NV>(x, w, K, Y, dev, st);
 }
 
