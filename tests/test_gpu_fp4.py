@@ -154,7 +154,7 @@ def values(t, fmt, g):
     return orc.quantize(f32(t), fmt, None if g is None else np.float32(g.item()))[2]
 
 
-CASES = [(1, 8, 32), (1, 128, 256), (2, 136, 64), (7, 264, 320), (16, 512, 1024), (17, 128, 96), (33, 392, 4096),
+CASES = [(1, 8, 32), (1, 128, 256), (2, 136, 64), (7, 264, 320), (16, 512, 1024), (17, 128, 96), (33, 392, 4096), (128, 264, 6176), (100, 72, 8256), (17, 1032, 8448),
          (64, 72, 2048), (65, 1000, 512), (128, 256, 288), (129, 264, 320), (300, 520, 1184), (257, 8, 4096),
          (515, 768, 2048),
          # few tokens: K split over the ranks of a cluster, ranks with uneven and with no parts, K past what is

@@ -34,20 +34,26 @@ constexpr int kKStage = 256;         // K values per stage: 128 bytes of codes p
 constexpr int kSfTile = 512;         // bytes of a scale tile: 128 rows x 4 blocks
 constexpr int kATile = 128 * 128;    // bytes of A per stage
 constexpr int kThreads = 192;        // producer, issuer, four epilogue warps
+constexpr int kHalfSmem = 113 * 1024;  // two CTAs on an SM: shared memory and
+constexpr int kHalfTmem = 256;         // tensor-memory columns of each
 
-template <int NT, bool NV>
+// DEEP: a CTA has its SM for itself; otherwise two share it.
+template <int NT, bool NV, bool DEEP>
 struct Cfg {
     static constexpr int SF = NV ? 4 : 2;              // scale tiles of a stage per 128 rows
     static constexpr int KSF = NV ? 64 : 128;          // K values of a scale tile
     static constexpr int BTILE = NT * 128;
     static constexpr int STAGE = kATile + BTILE + 2 * SF * kSfTile;
-    static constexpr int STAGES = NT >= 128 ? 6 : NT >= 64 ? 7 : 8;
+    static constexpr int FIT = ((DEEP ? 232448 : kHalfSmem) - 1280) / STAGE;
+    static constexpr int STAGES = FIT < 8 ? FIT : 8;   // 6 to 8 deep, 3 to 5
+    static constexpr int TMEM = DEEP ? 512 : kHalfTmem;
     static constexpr int SMEM = 1024 + STAGES * STAGE + 256;
+    static constexpr int PART = 128 * NT * 4;          // a CTA's part of the sums, in the stages' place
     static constexpr int ACC = NT < 32 ? 32 : NT;      // accumulator columns
     static constexpr int SF_COLS = 2 * SF * 4;         // scale columns of a stage
     static_assert(NT <= 128, "one scale tile covers the rows of B");
-    static_assert(ACC + STAGES * SF_COLS <= 512, "tensor memory columns");
-    static_assert(SMEM <= 232448, "shared memory");
+    static_assert(ACC + STAGES * SF_COLS <= TMEM, "tensor memory columns");
+    static_assert(STAGES >= 3 && PART <= STAGES * STAGE, "shared memory");
     static_assert(STAGE % 1024 == 0, "swizzled tiles start on 1024 bytes");
 };
 
@@ -65,6 +71,7 @@ struct Args {
     int K;
     const float *ga, *gb;       // tensor scales (nullable)
     __nv_bfloat16 *Y;           // [rows_b, rows_a]
+    int ranks;                  // CTAs of a cluster, which split K
     int *err;
     uint64_t wait_limit_ns;
 };
@@ -144,15 +151,19 @@ __device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, float (&v)[16]) {
 // (2^100 each) where the sum is 0.
 __device__ __forceinline__ float scaled(float sum, float ga, float gb) { return __fmul_rn(__fmul_rn(sum, ga), gb); }
 
-template <int NT, bool NV>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int NT, bool NV, bool DEEP>
+__global__ void __launch_bounds__(kThreads, DEEP ? 1 : 2)
     k_gemm_fp4(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Args p) {
-    using C = Cfg<NT, NV>;
+    using C = Cfg<NT, NV, DEEP>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
     Ctl *ctl = reinterpret_cast<Ctl *>(smem + C::STAGES * C::STAGE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // known to the compiler where there is one rank: with the join's code in it, this kernel
+    // drained 128 tokens of one rank 2 us more slowly
+    const int nranks = DEEP ? 1 : p.ranks, rank = DEEP ? 0 : static_cast<int>(blockIdx.x) % nranks;
+    float *part = reinterpret_cast<float *>(smem);  // once all MMAs have read the stages
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(&ctl->full[i], 1);
@@ -168,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     if (threadIdx.x == 0) pdl_allow_dependents();
     if (warp == 2) {
-        tmem_alloc(&ctl->tmem_base, 512);
+        tmem_alloc(&ctl->tmem_base, C::TMEM);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -176,16 +187,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
     volatile int *abort_flag = &ctl->abort_flag;
-    const int ta = blockIdx.x;
-    const int nkb = (p.K + kKStage - 1) / kKStage;
-
+    const int ta = blockIdx.x / nranks;
+    // this rank's stages: [kb0, kb1)
+    const int nkb = (p.K + kKStage - 1) / kKStage, per = (nkb + nranks - 1) / nranks;
+    const int kb0 = min(rank * per, nkb), kb1 = min(kb0 + per, nkb);
     if (warp == 0) {
         if (elect_one_sync()) {
             uint32_t armed = 0, armed_parity = 0;
             bool ok = true;
-            for (int kb = 0; kb < nkb; ++kb) {
-                const int st = kb % C::STAGES;
-                const uint32_t ph = (kb / C::STAGES) & 1u;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const int st = (kb - kb0) % C::STAGES;
+                const uint32_t ph = ((kb - kb0) / C::STAGES) & 1u;
                 if (!mbar_wait_bounded(&ctl->empty[st], ph ^ 1u, abort_flag, p.err, p.wait_limit_ns)) {
                     ok = false;
                     break;
@@ -217,9 +229,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         if (elect_one_sync()) {
             bool ok = true;
-            for (int kb = 0; kb < nkb; ++kb) {
-                const int st = kb % C::STAGES;
-                const uint32_t ph = (kb / C::STAGES) & 1u;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                const int st = (kb - kb0) % C::STAGES;
+                const uint32_t ph = ((kb - kb0) / C::STAGES) & 1u;
                 if (!mbar_wait_bounded(&ctl->full[st], ph, abort_flag, p.err, p.wait_limit_ns)) {
                     ok = false;
                     break;
@@ -242,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int j = NV ? kk : kk >> 1;
                     const uint32_t id = NV ? 0u : (kk & 1) * 2u;
                     mma_fp4<NV>(tmem, ad, bd, idesc_fp4(NT, NV, id), tsf + j * 4, tsf + C::SF * 4 + j * 4,
-                                (kb > 0 || kk > 0) ? 1u : 0u);
+                                (kb > kb0 || kk > 0) ? 1u : 0u);
                 }
                 tc_commit(&ctl->empty[st]);
             }
@@ -263,24 +275,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool ok = mbar_wait_bounded(&ctl->acc_full, 0, abort_flag, p.err, p.wait_limit_ns);
         if (__all_sync(0xffffffffu, ok)) {
             tc_fence_after();
-            const int64_t row = static_cast<int64_t>(ta) * 128 + quad * 32 + lane;
+            const int row = quad * 32 + lane;
+            const int64_t n = static_cast<int64_t>(ta) * 128 + row;
             const uint32_t taddr = tmem + ((quad * 32) << 16);
+            if (nranks > 1) {  // a rank without stages has made no MMA: its part is 0
 #pragma unroll 1
-            for (int c0 = 0; c0 < NT; c0 += 16) {
-                float v[16];
-                tmem_ld_16cols(taddr + c0, v);
-                if (row >= p.rows_a) continue;
+                for (int c0 = 0; c0 < NT; c0 += 16) {
+                    float v[16];
+                    tmem_ld_16cols(taddr + c0, v);
 #pragma unroll
-                for (int j = 0; j < 16; ++j)  // a warp's 32 rows are 32 neighbours of a row of Y
-                    if (c0 + j < p.rows_b) p.Y[(c0 + j) * p.rows_a + row] = __float2bfloat16_rn(scaled(v[j], ga, gb));
+                    for (int j = 0; j < 16; ++j) part[(c0 + j) * 128 + row] = kb1 > kb0 ? v[j] : 0.0f;
+                }
+            } else {
+#pragma unroll 1
+                for (int c0 = 0; c0 < NT; c0 += 16) {
+                    float v[16];
+                    tmem_ld_16cols(taddr + c0, v);
+                    if (n >= p.rows_a) continue;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)  // a warp's 32 rows are 32 neighbours of a row of Y
+                        if (c0 + j < p.rows_b)
+                            p.Y[(c0 + j) * p.rows_a + n] = __float2bfloat16_rn(scaled(v[j], ga, gb));
+                }
             }
         }
     }
     tc_fence_before();
+    if (nranks > 1) {
+        // the parts are complete in every CTA of the cluster
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+        const float ga = p.ga ? __ldg(p.ga) : 1.0f, gb = p.gb ? __ldg(p.gb) : 1.0f;
+        // a warp sums the 128 rows of four tokens at a time, in the order of the ranks
+        const int64_t n = static_cast<int64_t>(ta) * 128 + 4 * lane;  // rows are a multiple of 8
+        constexpr int kStep = kThreads / 32;
+        for (int m0 = rank + nranks * warp; m0 < p.rows_b; m0 += 4 * nranks * kStep) {
+            float4 sum[4] = {};
+#pragma unroll 4
+            for (int q = 0; q < nranks; ++q) {
+                float4 x[4] = {};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int m = m0 + i * nranks * kStep;
+                    if (m < p.rows_b)
+                        asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                     : "=f"(x[i].x), "=f"(x[i].y), "=f"(x[i].z), "=f"(x[i].w)
+                                     : "r"(map_to_rank(&part[m * 128 + 4 * lane], static_cast<uint32_t>(q))));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    sum[i].x = __fadd_rn(sum[i].x, x[i].x);
+                    sum[i].y = __fadd_rn(sum[i].y, x[i].y);
+                    sum[i].z = __fadd_rn(sum[i].z, x[i].z);
+                    sum[i].w = __fadd_rn(sum[i].w, x[i].w);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = m0 + i * nranks * kStep;
+                if (m < p.rows_b && n < p.rows_a)
+                    *reinterpret_cast<uint2 *>(p.Y + m * p.rows_a + n) =
+                        make_uint2(pack_bf16x2(scaled(sum[i].x, ga, gb), scaled(sum[i].y, ga, gb)),
+                                   pack_bf16x2(scaled(sum[i].z, ga, gb), scaled(sum[i].w, ga, gb)));
+            }
+        }
+        // no CTA leaves while another may read its part
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
     __syncthreads();
     if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc(tmem, C::TMEM);
     }
 }
 
@@ -636,17 +700,21 @@ struct DecCfg {
                   "two blocks per SM");
 };
 
-// Ranks that split K: enough for the slice that a CTA can pack, then doubled while every
-// SM has one CTA at most (and every rank two stages), or two of at least eight stages.
-// On 11008 x 4096 (86 tiles) two ranks take 7.9 us for one token where one takes 9.9.
-int decode_ranks(int64_t N, int64_t K) {
-    const int64_t tiles = (N + 127) / 128, stages = (K + kKStage - 1) / kKStage;
-    int ranks = 1;
-    while (static_cast<int64_t>(ranks) * kDecMaxSlice < K && ranks < 16) ranks *= 2;
-    while (ranks < 8 && ((2 * ranks * tiles <= kDecSms && stages >= 4 * ranks) ||
-                         (2 * ranks * tiles <= 2 * kDecSms && stages >= 16 * ranks)))
+// Doubles the ranks that split K while every SM has one CTA at most and every rank `least`
+// stages, or (`two`) two CTAs of at least eight stages.  On 11008 x 4096 (86 tiles) two ranks
+// take 7.9 us for one token where one takes 9.9.
+int split_ranks(int64_t tiles, int64_t stages, int ranks, int sms, int least, bool two) {
+    while (ranks < 8 && ((2 * ranks * tiles <= sms && stages >= 2 * least * ranks) ||
+                         (two && 2 * ranks * tiles <= 2 * sms && stages >= 16 * ranks)))
         ranks *= 2;
     return ranks;
+}
+
+// Enough ranks for the slice that a CTA can pack, at least.
+int decode_ranks(int64_t N, int64_t K) {
+    int ranks = 1;
+    while (static_cast<int64_t>(ranks) * kDecMaxSlice < K && ranks < 16) ranks *= 2;
+    return split_ranks((N + 127) / 128, (K + kKStage - 1) / kKStage, ranks, kDecSms, 2, true);
 }
 int64_t decode_slice(int64_t N, int64_t K) {
     const int64_t stages = (K + kKStage - 1) / kKStage, ranks = decode_ranks(N, K);
@@ -660,6 +728,7 @@ struct DecArgs {
     __nv_bfloat16 *Y;
     int64_t sf_tiles_k, N, K;
     int M, slice;  // K values per rank, a multiple of kKStage
+    int ranks;     // CTAs of a cluster
     int *err;
     uint64_t wait_limit_ns;
 };
@@ -710,9 +779,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_decode_fp4(const __grid_cons
     DecCtl *ctl = reinterpret_cast<DecCtl *>(xs + C::XSTAGES * C::SF * kSfTile);
     float *red = reinterpret_cast<float *>(smem);  // once all MMAs have read the stages
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint32_t rank, nranks;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(nranks));
+    const uint32_t nranks = static_cast<uint32_t>(p.ranks), rank = blockIdx.x % nranks;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kDecStages; ++i) {
             mbar_init(&ctl->full[i], 1);
@@ -854,15 +921,25 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_decode_fp4(const __grid_cons
     }
 }
 
+cudaLaunchAttribute cluster_of(int ranks) {
+    cudaLaunchAttribute cluster{};
+    cluster.id = ranks > 1 ? cudaLaunchAttributeClusterDimension : cudaLaunchAttributeIgnore;
+    cluster.val.clusterDim.x = static_cast<unsigned>(ranks);
+    cluster.val.clusterDim.y = 1;
+    cluster.val.clusterDim.z = 1;
+    return cluster;
+}
+
 struct Side {
     const uint8_t *codes, *scales;
     const float *g;
     int64_t rows;
 };
 
-template <int NT, bool NV>
-cudaError_t launch_t(const Side &a, const Side &b, int64_t K, void *Y, const DeviceInfo &dev, cudaStream_t st) {
-    using C = Cfg<NT, NV>;
+template <int NT, bool NV, bool DEEP>
+cudaError_t launch_t(const Side &a, const Side &b, int64_t K, int ranks, void *Y, const DeviceInfo &dev,
+                     cudaStream_t st) {
+    using C = Cfg<NT, NV, DEEP>;
     CUtensorMap ma, mb;
     cudaError_t e = encode_map_2d(ma, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.codes, K / 2, a.rows, K / 2, 128, 128,
                                   CU_TENSOR_MAP_SWIZZLE_128B);
@@ -870,7 +947,7 @@ cudaError_t launch_t(const Side &a, const Side &b, int64_t K, void *Y, const Dev
     e = encode_map_2d(mb, CU_TENSOR_MAP_DATA_TYPE_UINT8, b.codes, K / 2, b.rows, K / 2, 128, NT,
                       CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    auto kern = k_gemm_fp4<NT, NV>;
+    auto kern = k_gemm_fp4<NT, NV, DEEP>;
     static std::atomic<uint64_t> done{0};
     const uint64_t bit = 1ull << (dev.device & 63);
     if (!(done.load() & bit)) {
@@ -884,6 +961,7 @@ cudaError_t launch_t(const Side &a, const Side &b, int64_t K, void *Y, const Dev
     p.sf_tiles_k = (K / (NV ? 16 : 32) + 3) / 4;
     p.rows_a = a.rows;
     p.rows_b = b.rows;
+    p.ranks = ranks;
     p.K = static_cast<int>(K);
     p.ga = a.g;
     p.gb = b.g;
@@ -892,7 +970,8 @@ cudaError_t launch_t(const Side &a, const Side &b, int64_t K, void *Y, const Dev
     if (!p.err) return cudaErrorInvalidSymbol;
     p.wait_limit_ns = kWaitLimitNs;
     const int64_t tiles = (a.rows + 127) / 128;  // rows are below 2^31
-    return launch_pdl(kern, dim3(static_cast<unsigned>(tiles)), dim3(kThreads), C::SMEM, st, ma, mb, p);
+    return launch_pdl_ex(kern, dim3(static_cast<unsigned>(tiles * ranks)), dim3(kThreads), C::SMEM, st,
+                         cluster_of(ranks), ma, mb, p);
 }
 
 template <bool NV>
@@ -942,13 +1021,27 @@ cudaError_t launch_pair(const Side &a, const Side &b, int64_t K, void *Y, const 
     return launch_pdl(kern, dim3(grid), dim3(kPairThreads), C::SMEM, st, ma, mb, sa, sb, my, p);
 }
 
+// Up to 128 tokens: from eight stages on, K is split over the ranks of a cluster (64 tokens
+// of 4096 x 4096 take 9.2 us where one rank takes 11.5; on 1024 x 1024, four stages, two ranks
+// take 7.4 where one takes 6.8).  The join of 128 columns costs more: such ranks have four
+// stages, and do not share an SM.  One rank has the deep ring if it has its SM for itself (its
+// three stages took 2 us more for 128 tokens of 1024 x 1024); clusters do not, since an SM may then hold two of their CTAs (16 clusters of 8 do not find
+// 8 free SMs in a group each: 17 tokens of 2048 x 8192 13.4 us against 9.3).
+template <int NT, bool NV>
+cudaError_t launch_few(const Side &w, const Side &x, int64_t K, void *Y, const DeviceInfo &dev, cudaStream_t st) {
+    const int64_t tiles = (w.rows + 127) / 128, stages = (K + kKStage - 1) / kKStage;
+    const int ranks = stages < 8 ? 1 : split_ranks(tiles, stages, 1, dev.sm_count, NT <= 64 ? 2 : 4, NT <= 64);
+    return ranks == 1 && tiles <= dev.sm_count ? launch_t<NT, NV, true>(w, x, K, ranks, Y, dev, st)
+                                               : launch_t<NT, NV, false>(w, x, K, ranks, Y, dev, st);
+}
+
 template <bool NV>
 cudaError_t dispatch(const Side &x, const Side &w, int64_t K, void *Y, const DeviceInfo &dev, cudaStream_t st) {
     const int64_t M = x.rows;
-    if (M <= 16) return launch_t<16, NV>(w, x, K, Y, dev, st);
-    if (M <= 32) return launch_t<32, NV>(w, x, K, Y, dev, st);
-    if (M <= 64) return launch_t<64, NV>(w, x, K, Y, dev, st);
-    if (M <= 128) return launch_t<128, NV>(w, x, K, Y, dev, st);
+    if (M <= 16) return launch_few<16, NV>(w, x, K, Y, dev, st);
+    if (M <= 32) return launch_few<32, NV>(w, x, K, Y, dev, st);
+    if (M <= 64) return launch_few<64, NV>(w, x, K, Y, dev, st);
+    if (M <= 128) return launch_few<128, NV>(w, x, K, Y, dev, st);
     return launch_pair<NV>(x, w, K, Y, dev, st);
 }
 
@@ -981,25 +1074,24 @@ cudaError_t launch_decode(const void *X, const float *gx, const Side &w, int64_t
     p.N = w.rows;
     p.K = K;
     p.M = static_cast<int>(M);
+    p.ranks = ranks;
     p.slice = static_cast<int>(decode_slice(w.rows, K));
     p.err = device_error_word();
     if (!p.err) return cudaErrorInvalidSymbol;
     p.wait_limit_ns = kWaitLimitNs;
-    cudaLaunchAttribute cluster{};
-    cluster.id = cudaLaunchAttributeClusterDimension;
-    cluster.val.clusterDim.x = static_cast<unsigned>(ranks);
-    cluster.val.clusterDim.y = 1;
-    cluster.val.clusterDim.z = 1;
-    return launch_pdl_ex(kern, dim3(static_cast<unsigned>(tiles * ranks)), dim3(kDecThreads), C::SMEM, st, cluster, map, p);
+    return launch_pdl_ex(kern, dim3(static_cast<unsigned>(tiles * ranks)), dim3(kDecThreads), C::SMEM, st,
+                         cluster_of(ranks), map, p);
 }
 
 }  // namespace
 
-// The product packs X itself while that is little work for a CTA: 16 tokens by 1024 values
-// or 8 by 2048 (16 by 4096 took 21.5 us on 11008 x 4096, a packing kernel and the plain
-// product 12.0).
+// The product packs X itself while that is little work for a CTA, 8 tokens by 1024 values
+// or 4 by 2048, and no second wave of CTAs does it again.  At the border both ways take
+// the same (8 tokens on 4096 x 4096 7.7 us, 9 packed apart 8.0); 1 token on 28672 x 8192, 896
+// CTAs, took 32.0 us where packing apart takes 27.
 bool fp4_packs_in_product(int64_t M, int64_t N, int64_t K) {
-    return M <= kDecTokens && K <= 8ll * kDecMaxSlice && M * decode_slice(N, K) <= 16 * 1024;
+    return M <= kDecTokens && K <= 8ll * kDecMaxSlice && M * decode_slice(N, K) <= 8 * 1024 &&
+           (N + 127) / 128 * decode_ranks(N, K) <= 2 * kDecSms;
 }
 
 cudaError_t launch_fp4_few_tokens(const void *X, const float *gx, const uint8_t *w_codes, const uint8_t *w_scales,
