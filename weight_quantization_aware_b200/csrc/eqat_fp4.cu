@@ -1,8 +1,12 @@
 // Microscaled 4-bit floats: packing, fake quantization, reading back and the tensor scale
 // (the formats and their element arithmetic are in eqat_fp4.cuh).
 //
-// Every kernel here is HBM-bound: a thread takes 16 values (two 16-byte loads of bf16), a
-// warp 512 consecutive values of a row.
+// Every kernel here is meant to be HBM-bound: a thread takes 16 values (two 16-byte loads
+// of bf16), a warp 512 consecutive values of a row, the next of which are on their way
+// while one is encoded.  Measured on 28672 x 8192 bf16 (a copy runs at 6.55 TB/s): tensor
+// scale 75 us (6.3 TB/s), pack mx 100 us (5.9) and nv 136 us (4.4), fake quantization mx 164
+// and nv 168 us (5.7, 5.6), values from codes 111 us (5.4).  nv packing is bound by
+// instruction issue: the exact division by the block's scale.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

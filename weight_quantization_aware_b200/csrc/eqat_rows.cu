@@ -17,6 +17,11 @@
 // What bounds the first walk besides memory is ex2 (a quarter of the issue rate), then
 // instruction issue: one packed-fp32 instruction does two entries of each step.
 //
+// Measured, bf16 (a copy runs at 6.55 TB/s): log probabilities of 2048 x 32000 29.5 us (4.4
+// TB/s) and of 1024 x 131072 49.8 us (5.4 TB/s), with 64 alternatives 67 and 84 us; the
+// distillation step of 2048 x 32000 with 64 slots 73 us (3.6 TB/s; the block meets at
+// two barriers between a row's walks) and the gradient alone of 2048 x 131072 214 us (5.0 TB/s).
+//
 // All sums are fp32 per thread (a few hundred terms of one sign), joined over the
 // block in a fixed order; the few values per row (log S, the loss) are fp64.
 #include <cuda_bf16.h>
