@@ -19,7 +19,7 @@
 //
 // Measured, bf16 (a copy runs at 6.55 TB/s): log probabilities of 2048 x 32000 29.5 us (4.4
 // TB/s) and of 1024 x 131072 49.8 us (5.4 TB/s), with 64 alternatives 67 and 84 us; the
-// distillation step of 2048 x 32000 with 64 slots 73 us (3.6 TB/s; the block meets at
+// distillation step of 2048 x 32000 with 64 slots 71 us (3.7 TB/s; the block meets at
 // two barriers between a row's walks) and the gradient alone of 2048 x 131072 214 us (5.0 TB/s).
 //
 // All sums are fp32 per thread (a few hundred terms of one sign), joined over the
@@ -154,9 +154,11 @@ struct Vec<__nv_bfloat16> {
     // elements j with bit j set become -inf
     static __device__ __forceinline__ void fill(uint4 &r, uint32_t bits) {
         auto word = [&](uint32_t w, int i) {
-            const uint32_t lo = (bits >> (2 * i)) & 1u ? 0xFF80u : w & 0xFFFFu;
-            const uint32_t hi = (bits >> (2 * i + 1)) & 1u ? 0xFF800000u : w & 0xFFFF0000u;
-            return lo | hi;
+            // bits 2 i and 2 i + 1 to the signs of bytes 0 and 1, and from there to halves
+            const uint32_t sign = ((bits >> (2 * i)) & 1u) * 0x80u | ((bits >> (2 * i)) & 2u) * 0x4000u;
+            uint32_t m;
+            asm("prmt.b32 %0, %1, 0, 0x9988;" : "=r"(m) : "r"(sign));
+            return (w & ~m) | (kNegInfBf16x2 & m);
         };
         r = make_uint4(word(r.x, 0), word(r.y, 1), word(r.z, 2), word(r.w, 3));
     }
@@ -1234,10 +1236,12 @@ __global__ void __launch_bounds__(W + 64, kCtasPerSm<W>) k_distill(const Distill
         const bool skip = w == 0.0f;  // a token without a loss: nothing of its row is read
         if (walker && !skip) {
             Sums<false> mine(a.c);
-            // slots are left out of the sums
+            // slots are left out of the sums (a vector's bits are a byte of the bitmap, or half
+            // of one)
+            const uint8_t *bytes = reinterpret_cast<const uint8_t *>(bitmap);
             auto mask = [&](uint4 &r, int v) {
-                const int at = v * Vec<T>::N;
-                const uint32_t bits = (bitmap[at >> 5] >> (at & 31)) & ((1u << Vec<T>::N) - 1u);
+                uint32_t bits = bytes[static_cast<uint32_t>(v) * Vec<T>::N / 8];
+                if (Vec<T>::N == 4) bits = (v & 1) ? bits >> 4 : bits & 15u;
                 if (bits) Vec<T>::fill(r, bits);
             };
             ring_walk<W>(row, ring, ctl, pos, a.err, [&](uint4(&r)[kUnroll], int v, int n) {
