@@ -154,7 +154,8 @@ def values(t, fmt, g):
     return orc.quantize(f32(t), fmt, None if g is None else np.float32(g.item()))[2]
 
 
-CASES = [(1, 8, 32), (1, 128, 256), (2, 136, 64), (7, 264, 320), (16, 512, 1024), (17, 128, 96), (33, 392, 4096), (128, 264, 6176), (100, 72, 8256), (17, 1032, 8448),
+CASES = [(1, 8, 32), (1, 128, 256), (2, 136, 64), (7, 264, 320), (16, 512, 1024), (17, 128, 96), (33, 392, 4096),
+         (128, 264, 6176), (100, 72, 8256), (17, 1032, 8448),
          (64, 72, 2048), (65, 1000, 512), (128, 256, 288), (129, 264, 320), (300, 520, 1184), (257, 8, 4096),
          (515, 768, 2048),
          # few tokens: K split over the ranks of a cluster, ranks with uneven and with no parts, K past what is
@@ -295,3 +296,35 @@ def test_a_distillation_step_through_a_packed_output_layer():
     for got, a, b, n in ((dX, dy, wv, V), (dW, dy.T, xv, M)):
         ref, mag = a @ b, np.abs(a) @ np.abs(b)
         assert (np.abs(f32(got) - ref) <= 2.0 ** -8 * np.abs(ref) + (n / 16 + 8) * 2.0 ** -22 * mag).all()
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_matrices_past_32_bit_offsets(fmt):
+    """More than 2^31 values: the last rows are what packing and multiplying them alone gives."""
+    N, K = 65544, 32768
+    W = torch.empty(N, K, dtype=torch.bfloat16, device="cuda")
+    W[: N - 8] = 0.25
+    W[N - 8:] = draw(8, K, torch.bfloat16, 5).cuda()
+    tail = W[N - 8:].clone()
+    g = None
+    if fmt == "nv":
+        g = eqat.fp4_tensor_scale(W)
+        assert torch.equal(g, eqat.fp4_tensor_scale(torch.cat([tail, W[:1]])))
+    codes, scales = eqat.pack_fp4(W, fmt, tscale=g)
+    want = eqat.fake_quant_fp4(tail, fmt, tscale=g)
+    assert torch.equal(eqat.fake_quant_fp4(W, fmt, tscale=g, W_hat=W)[N - 8:], want)
+    assert torch.equal(W[N - 9], eqat.fake_quant_fp4(torch.full((1, K), 0.25, dtype=torch.bfloat16, device="cuda"), fmt,
+                                                     tscale=g)[0])
+    W.zero_()
+    assert torch.equal(eqat.dequant_fp4(codes, scales, fmt, tscale=g, out=W)[N - 8:], want)
+    del W
+    wv = f32(want).astype(np.float64)
+    for M in (3, 40, 130):
+        X = draw(M, K, torch.bfloat16, M, 1.0)
+        gx = scale_of(X, fmt)
+        Y = eqat.fp4_linear_fwd(X.cuda(), codes, scales, fmt, tscale=g, x_tscale=gx)
+        xv = values(X, fmt, gx)
+        ref, mag = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+        bound = 2.0 ** -8 * np.abs(ref) + (K / 64 + 8) * 2.0 ** -22 * mag + 1e-37
+        assert (np.abs(f32(Y[:, N - 8:]) - ref) <= bound).all()
+        assert torch.equal(Y[:, 0], Y[:, N - 9])  # equal rows of W, the first and the last of them

@@ -5,7 +5,9 @@ fp32 sums and the block joins 512 of them in 13 steps, so S has a relative error
 most (V / 512 + 16) 2^-24 from the additions; each term 2^y carries 2^-22 from ex2 and,
 from two roundings of y, |y| 2^-23 ln 2, which weighted by 2^y stays below 2^-23.  So
 ln S is within tol(V) = (V / 512 + 32) 2^-24 + 2^-21, absolutely.  Values that are
-rounded to fp32 at the end add 2^-24 of themselves.
+rounded to fp32 at the end add 2^-24 of themselves.  (On short rows, V <= 16384, a thread
+of the narrow block adds up to V / 128 terms: of either sign and half an ulp of a growing
+sum at most, 128 roundings stay within 16 2^-24 at four standard deviations.)
 """
 import numpy as np
 import pytest
@@ -387,3 +389,33 @@ def test_rows_on_a_side_stream_and_in_a_captured_graph():
         assert torch.equal(a, b)
     l2, g2 = eqat.distill_topk_step(x, again[2], again[3], tail=True)
     assert torch.equal(l, l2) and torch.equal(g, g2)
+
+
+def test_rows_past_32_bit_offsets():
+    """Rows that start 2^30 elements apart, and one of 2^28 + 3 entries."""
+    V, ld = 1001, 1 << 30
+    y = make(3, V, torch.bfloat16, 17)
+    x = torch.empty(2 * ld + V, dtype=torch.bfloat16, device="cuda").as_strided((3, V), (ld, 1))
+    x.copy_(y)
+    # rows that start as x's do, on 16 bytes: the order of the sums depends on it
+    y = torch.nn.functional.pad(y, (0, 7))[:, :V]
+    t = torch.tensor([1, 1000, 500], device="cuda")
+    for a, b in zip(eqat.token_logprobs(x, t, top_k=5), eqat.token_logprobs(y, t, top_k=5)):
+        assert torch.equal(a, b)
+    ids = torch.arange(4, device="cuda").repeat(3, 1)
+    tlp = torch.full((3, 4), -2.0, device="cuda")
+    want_l, want_g = eqat.distill_topk_step(y, ids, tlp, tail=True)
+    loss, grad = eqat.distill_topk_step(x, ids, tlp, tail=True, dlogits=x)
+    assert torch.equal(loss, want_l) and torch.equal(grad, want_g)
+    del x, grad
+    V = (1 << 28) + 3  # equal entries: all sums are whole numbers below 2^24 per thread, but the last
+    z = torch.zeros(1, V, dtype=torch.bfloat16, device="cuda")
+    z[0, V - 1], z[0, V - 2] = 2.0, 1.0
+    S = (V - 2) + np.exp(2.0) + np.exp(1.0)
+    for k in (0, 3):
+        lp, ent, ids, top = eqat.token_logprobs(z, torch.tensor([V - 1], device="cuda"), top_k=k)
+        # ln S near 19.4: three fp32 roundings of it, and 2^-20 of the sums' joins
+        assert abs(lp.item() - (2 - np.log(S))) < 1e-5
+        assert abs(ent.item() - (np.log(S) - (2 * np.exp(2.0) + np.exp(1.0)) / S)) < 5e-5
+    assert ids.tolist() == [[V - 1, V - 2, 0]]
+    assert abs(top[0, 2].item() + np.log(S)) < 1e-5
