@@ -328,3 +328,31 @@ def test_matrices_past_32_bit_offsets(fmt):
         bound = 2.0 ** -8 * np.abs(ref) + (K / 64 + 8) * 2.0 ** -22 * mag + 1e-37
         assert (np.abs(f32(Y[:, N - 8:]) - ref) <= bound).all()
         assert torch.equal(Y[:, 0], Y[:, N - 9])  # equal rows of W, the first and the last of them
+
+
+def test_calls_at_once_on_three_streams():
+    """Products of a few, some and many tokens and a distillation step, in flight together
+    on streams of their own: the same bits as alone."""
+    from weight_quantization_aware_b200 import distill_topk_step
+    W = draw(2056, 4096, torch.bfloat16, 6).cuda()
+    calls = []
+    for fmt, M in (("nv", 4), ("mx", 40), ("nv", 300)):
+        g = scale_of(W, fmt)
+        codes, scales = eqat.pack_fp4(W, fmt, tscale=g)
+        X = draw(M, 4096, torch.bfloat16, M, 1.0).cuda()
+        calls.append(lambda X=X, c=codes, s=scales, f=fmt, g=g: eqat.fp4_linear_fwd(X, c, s, f, tscale=g, x_tscale=g))
+    z = draw(500, 3001, torch.bfloat16, 7, 2.0).cuda()
+    ids = torch.arange(20, device="cuda").repeat(500, 1)
+    tlp = torch.full((500, 20), -4.0, device="cuda")
+    calls.append(lambda: distill_topk_step(z, ids, tlp, tail=True)[1])
+    want = [f() for f in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for i in range(60):
+        with torch.cuda.stream(streams[i % 3]):
+            j = (i // 2) % len(calls)
+            got.append((j, calls[j]()))
+    torch.cuda.synchronize()
+    for j, t in got:
+        assert torch.equal(t, want[j])
