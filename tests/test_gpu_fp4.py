@@ -178,6 +178,33 @@ def test_linear_fwd(case, fmt):
     assert (d <= bound).all(), f"worst {np.max(d / bound):.3f} of the bound"
 
 
+def check_product(M, N, K, fmt, repeats=1):
+    """Every element of Y against the oracle's packed values (their fp64 product is taken
+    on the GPU), every time the same bits."""
+    X, W = draw(M, K, torch.bfloat16, 1, 1.0), draw(N, K, torch.bfloat16, 2)
+    gx, gw = scale_of(X, fmt), scale_of(W, fmt)
+    codes, scales = packed(W, fmt, gw)
+    X = X.cuda()
+    Ys = [eqat.fp4_linear_fwd(X, codes, scales, fmt, tscale=gw, x_tscale=gx) for _ in range(repeats)]
+    xv, wv = (torch.from_numpy(v).cuda() for v in (values(X, fmt, gx), values(W, fmt, gw)))
+    ref, mag = xv @ wv.t(), xv.abs() @ wv.abs().t()
+    bound = 2.0 ** -8 * ref.abs() + (K / 64 + 8) * 2.0 ** -22 * mag + 1e-37
+    d = (Ys[0].double() - ref).abs()
+    assert bool((d <= bound).all()), f"worst {(d / bound).max().item():.3f} of the bound"
+    for Y in Ys[1:]:
+        assert torch.equal(Y, Ys[0])
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("rest", [8, 40, 104, 136, 168, 200, 224])
+def test_pair_product_of_ragged_widths(rest, fmt):
+    """The last tile along N ends inside: its chunks past Y are not stored, and the next
+    chunk's buffer must still be free.  With 31 x 4 and 41 x 4 tiles on 74 pairs that tile is a
+    pair's second and third: in either accumulator."""
+    for whole in (30, 40):
+        check_product(1000, 256 * whole + rest, 96, fmt, repeats=8)
+
+
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 @pytest.mark.parametrize("M", [3, 200])
 def test_linear_fwd_keeps_nan_blocks_to_their_rows(M, fmt):

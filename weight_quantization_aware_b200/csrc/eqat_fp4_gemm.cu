@@ -625,8 +625,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
             const int row0 = tm * 256 + static_cast<int>(rank) * 128 + quad * 32;
             const bool odd = local & 1u;
             const uint32_t taddr = tmem + ((quad * 32) << 16) + (odd ? kAcc1 : 0);
-            // 32 rows of 64 bytes, 16-byte units swizzled as the output map's box
+            // 32 rows of 64 bytes, 16-byte units swizzled as the output map's box.  A chunk that
+            // lies outside Y takes no buffer: chunks and bulk groups are counted alike, so that
+            // "all groups but the last" are those of this chunk's buffer.
             auto put = [&](const float *v, int c0) {
+                if (row0 >= p.rows_a || tn * 256 + c0 >= p.rows_b) return;
                 uint8_t *dst = buf + (chunk++ & 1) * 2048;
                 if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                 __syncwarp();
@@ -642,7 +645,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 // the map clips a chunk at the matrix's end
-                if (lane == 0 && row0 < p.rows_a && tn * 256 + c0 < p.rows_b) tma_store_2d(&tmY, dst, tn * 256 + c0, row0);
+                if (lane == 0) tma_store_2d(&tmY, dst, tn * 256 + c0, row0);
             };
             // The columns that the next tile's accumulator overlaps go to registers first,
             // and its MMAs may start; then they are written, and the rest follows.
