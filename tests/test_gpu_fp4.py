@@ -206,6 +206,31 @@ def test_pair_product_of_ragged_widths(rest, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("M,N,K", [(2060, 5128, 64), (2060, 5128, 256), (2060, 5128, 288), (1300, 8200, 1312),
+                                   (150, 40000, 544), (5000, 2056, 32)])
+def test_pair_product_of_several_tiles_per_pair(M, N, K, fmt):
+    """More than twice as many tiles as pairs: accumulators taken in turn, whose overlapping
+    columns are handed over, and scale buffers that go on from tile to tile; contractions
+    shorter than the drain of a tile and longer."""
+    check_product(M, N, K, fmt, repeats=3)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_packing_of_several_segments_per_warp(dtype, fmt):
+    """Four times as many segments as warps, the second of a row ragged: what is fetched
+    ahead is the next segment's, in place too."""
+    N, K = 20001, 544
+    W = draw(N, K, dtype, 11)
+    g = None if fmt == "mx" else 2.0 ** -12
+    check_pack(W, fmt, g)
+    gd = None if g is None else torch.tensor([g], device="cuda")
+    Wd = W.cuda()
+    want = eqat.fake_quant_fp4(Wd, fmt, tscale=gd)  # just compared with the oracle
+    assert eqat.fake_quant_fp4(Wd, fmt, tscale=gd, W_hat=Wd) is Wd and torch.equal(Wd, want)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
 @pytest.mark.parametrize("M", [3, 200])
 def test_linear_fwd_keeps_nan_blocks_to_their_rows(M, fmt):
     N, K = 136, 192
