@@ -106,6 +106,23 @@ def test_largest_tensor_scales(M):
     assert np.array_equal(Y, want)
 
 
+@pytest.mark.parametrize("M", [2, 13, 40, 150])
+@pytest.mark.parametrize("ex", [100, -100])
+def test_tensor_scales_of_opposite_sizes(M, ex):
+    """2^100 on one side and 2^-100 on the other: sums near 2^30 and 2 stay what they are,
+    whichever scale comes first."""
+    K = 256
+    gx, gw = (torch.full((1,), 2.0 ** e, device="cuda") for e in (ex, -ex))
+    X = torch.full((M, K), 2688.0 * 2.0 ** ex, dtype=torch.bfloat16, device="cuda")
+    W = torch.full((136, K), 2688.0 * 2.0 ** -ex, dtype=torch.bfloat16, device="cuda")
+    X[1], W[5] = 6 * 2.0 ** (ex - 6), 6 * 2.0 ** (-ex - 6)  # a block scale of 2^-6 and codes of 6
+    codes, scales = eqat.pack_fp4(W, "nv", tscale=gw)
+    Y = eqat.fp4_linear_fwd(X, codes, scales, "nv", tscale=gw, x_tscale=gx)
+    x, w = torch.full((M, 1), 2688.0, dtype=torch.float64), torch.full((136, 1), 2688.0, dtype=torch.float64)
+    x[1], w[5] = 6 / 64, 6 / 64
+    assert torch.equal(Y.cpu(), (K * x @ w.t()).to(torch.bfloat16))  # all sums are exact in fp32
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
 def test_any_tensor_scale(dtype):
     """A tensor scale that is not a power of two: the same fp32 operations in the same order."""

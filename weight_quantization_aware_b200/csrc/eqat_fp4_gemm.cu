@@ -150,9 +150,18 @@ __device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, float (&v)[16]) {
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// A sum and its tensor scales, one after the other: their product alone may be infinite
-// (2^100 each) where the sum is 0.
-__device__ __forceinline__ float scaled(float sum, float ga, float gb) { return __fmul_rn(__fmul_rn(sum, ga), gb); }
+// The tensor scales as the two factors of a sum.  Scales on either side of 1 are one
+// factor, which lies between them: a sum times 2^100 may be infinite where 2^-100 would
+// bring it back.  Others stay two: their product may be infinite (2^100 each) where the sum is 0.
+struct Factors {
+    float a, b;
+};
+__device__ __forceinline__ Factors tensor_factors(const float *ga, const float *gb) {
+    const float a = ga ? __ldg(ga) : 1.0f, b = gb ? __ldg(gb) : 1.0f;
+    if ((a > 1.0f) != (b > 1.0f)) return Factors{__fmul_rn(a, b), 1.0f};
+    return Factors{a, b};
+}
+__device__ __forceinline__ float scaled(float sum, const Factors &g) { return __fmul_rn(__fmul_rn(sum, g.a), g.b); }
 
 template <int NT, bool NV, bool DEEP>
 __global__ void __launch_bounds__(kThreads, DEEP ? 1 : 2)
@@ -274,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : 2)
         __syncwarp();
     } else {
         const int quad = warp & 3;
-        const float ga = p.ga ? __ldg(p.ga) : 1.0f, gb = p.gb ? __ldg(p.gb) : 1.0f;
+        const Factors g = tensor_factors(p.ga, p.gb);
         const bool ok = mbar_wait_bounded(&ctl->acc_full, 0, abort_flag, p.err, p.wait_limit_ns);
         if (__all_sync(0xffffffffu, ok)) {
             tc_fence_after();
@@ -298,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : 2)
 #pragma unroll
                     for (int j = 0; j < 16; ++j)  // a warp's 32 rows are 32 neighbours of a row of Y
                         if (c0 + j < p.rows_b)
-                            p.Y[(c0 + j) * p.rows_a + n] = __float2bfloat16_rn(scaled(v[j], ga, gb));
+                            p.Y[(c0 + j) * p.rows_a + n] = __float2bfloat16_rn(scaled(v[j], g));
                 }
             }
         }
@@ -307,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : 2)
     if (nranks > 1) {
         // the parts are complete in every CTA of the cluster
         asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-        const float ga = p.ga ? __ldg(p.ga) : 1.0f, gb = p.gb ? __ldg(p.gb) : 1.0f;
+        const Factors g = tensor_factors(p.ga, p.gb);
         // a warp sums the 128 rows of four tokens at a time, in the order of the ranks
         const int64_t n = static_cast<int64_t>(ta) * 128 + 4 * lane;  // rows are a multiple of 8
         constexpr int kStep = kThreads / 32;
@@ -337,8 +346,8 @@ __global__ void __launch_bounds__(kThreads, DEEP ? 1 : 2)
                 const int m = m0 + i * nranks * kStep;
                 if (m < p.rows_b && n < p.rows_a)
                     *reinterpret_cast<uint2 *>(p.Y + m * p.rows_a + n) =
-                        make_uint2(pack_bf16x2(scaled(sum[i].x, ga, gb), scaled(sum[i].y, ga, gb)),
-                                   pack_bf16x2(scaled(sum[i].z, ga, gb), scaled(sum[i].w, ga, gb)));
+                        make_uint2(pack_bf16x2(scaled(sum[i].x, g), scaled(sum[i].y, g)),
+                                   pack_bf16x2(scaled(sum[i].z, g), scaled(sum[i].w, g)));
             }
         }
         // no CTA leaves while another may read its part
@@ -615,7 +624,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
         // ---------------------------------------------------------- epilogue (both CTAs)
         const int quad = warp & 3;
         uint8_t *buf = out + quad * 4096;
-        const float ga = p.ga ? __ldg(p.ga) : 1.0f, gb = p.gb ? __ldg(p.gb) : 1.0f;
+        const Factors g = tensor_factors(p.ga, p.gb);
         uint32_t local = 0, chunk = 0;
         for (int t = pair; t < p.tiles; t += npairs, ++local) {
             const bool ok = mbar_wait_bounded(&ctl->acc_full, local & 1u, abort_flag, p.err, p.wait_limit_ns);
@@ -638,7 +647,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) __cluster_dims__(2, 1, 1)
                     uint32_t w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        w[j] = pack_bf16x2(scaled(v[8 * q + 2 * j], ga, gb), scaled(v[8 * q + 2 * j + 1], ga, gb));
+                        w[j] = pack_bf16x2(scaled(v[8 * q + 2 * j], g), scaled(v[8 * q + 2 * j + 1], g));
                     *reinterpret_cast<uint4 *>(dst + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
                         make_uint4(w[0], w[1], w[2], w[3]);
                 }
@@ -904,7 +913,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_decode_fp4(const __grid_cons
     tc_fence_before();
     // the parts are complete in every CTA of the cluster
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    const float gx = p.gx ? __ldg(p.gx) : 1.0f, gw = p.gw ? __ldg(p.gw) : 1.0f;
+    const Factors g = tensor_factors(p.gx, p.gw);
     const int rows = 128 / static_cast<int>(nranks);  // of this rank
     for (int i = threadIdx.x; i < rows * p.M; i += kDecThreads) {
         const int row = static_cast<int>(rank) * rows + i % rows, m = i / rows;
@@ -917,7 +926,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) k_decode_fp4(const __grid_cons
                          : "r"(map_to_rank(&red[row * (kDecTokens + 1) + m], q)));
             sum = __fadd_rn(sum, part);
         }
-        if (n < p.N) p.Y[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(scaled(sum, gx, gw));
+        if (n < p.N) p.Y[static_cast<int64_t>(m) * p.N + n] = __float2bfloat16_rn(scaled(sum, g));
     }
     // no CTA leaves while another may read its part
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
