@@ -365,6 +365,14 @@ eqat_status eqat_distill_topk(const void *x, int dt, int64_t ld, int64_t T, int6
                               const float *tlp, int k, double temperature, uint32_t flags, const float *weight,
                               float *loss, void *dx, eqat_stream_t stream);
 
+/* eqat_distill_topk with a row stride of dx's own: for logits that are a few rows of a
+ * large buffer (the last position of each sequence) dx need not be as large.  ld_dx >= V,
+ * and where T > 1 it agrees with ld modulo 16 bytes; it is ld where dx is x. */
+eqat_status eqat_distill_topk_strided(const void *x, int dt, int64_t ld, int64_t T, int64_t V, const int64_t *ids,
+                                      const float *tlp, int k, double temperature, uint32_t flags,
+                                      const float *weight, float *loss, void *dx, int64_t ld_dx,
+                                      eqat_stream_t stream);
+
 /* ------------------------------------------------------------------------------
  * Microscaled 4-bit floats
  *

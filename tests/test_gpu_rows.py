@@ -345,6 +345,45 @@ def test_distill_in_place_and_padding_left_alone(dtype):
     assert torch.equal(x, want) and torch.equal(wide[:, V:], pad)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_distill_gradient_of_rows_far_apart(dtype):
+    """The last position of each sequence of [B, S, V]: the gradient does not take the
+    parent's memory, and is the same bits at any of its strides."""
+    for B, S, V in ((5, 64, 1001), (9, 33, 3002), (3, 64, 70001)):
+        parent = torch.randn(B, S, V, device="cuda").to(dtype)
+        step = 16 // parent.element_size()
+        at = max(i for i in range(S) if i * V % step == 0)  # its first row starts on 16 bytes
+        x = parent[:, at]
+        ids, tlp = teacher(x, 8, 1)
+        w = torch.rand(B, device="cuda")
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        loss, grad = eqat.distill_topk_step(x, ids, tlp, weight=w, tail=True)
+        assert torch.cuda.max_memory_allocated() - before < 2 * B * (V + step) * x.element_size() + 8192
+        check_distill(x, ids, tlp, w, 1.0, True)
+        wide = torch.full((B, S * V), 7.0, dtype=dtype, device="cuda")  # logits' own stride
+        out = wide[:, :V]
+        assert eqat.distill_topk_bwd(x, ids, tlp, w, tail=True, dlogits=out) is out
+        assert torch.equal(out, grad) and bool((wide[:, V:] == 7.0).all())
+        with pytest.raises(ValueError):
+            eqat.distill_topk_bwd(x, ids, tlp, w, dlogits=torch.empty(B, S * V + 1, dtype=dtype, device="cuda")[:, :V])
+        eqat.distill_topk_bwd(x, ids, tlp, w, tail=True, dlogits=x)
+        assert torch.equal(x, grad)
+
+
+def test_distill_gradient_beside_the_logits():
+    """Logits and gradient as two halves of one buffer's rows."""
+    T, V = 40, 1000
+    both = torch.randn(T, 2 * V, device="cuda")
+    x, g = both[:, :V], both[:, V:]
+    ids, tlp = teacher(x, 8, 1)
+    w = torch.ones(T, device="cuda")
+    want = eqat.distill_topk_bwd(x, ids, tlp, w)
+    keep = x.clone()
+    eqat.distill_topk_bwd(x, ids, tlp, w, dlogits=g)
+    assert torch.equal(g, want) and torch.equal(x, keep)
+
+
 def test_distill_gradient_matches_differences():
     """The kernel's gradient against central differences of the kernel's own fp32 loss,
     summed along a random direction: h = 2^-4 leaves a third-order error of about

@@ -150,6 +150,24 @@ def test_distill_refusals(lib):
     assert distill(lib, T=0) == OK
 
 
+def test_distill_gradient_strides(lib):
+    """dx has a row stride of its own, which agrees with x's modulo 16 bytes."""
+    def call(x=FAKE, dx=FAKE + (1 << 20), ld=40, ld_dx=40, T=3, V=33, dt=1, loss=0, ids=FAKE):
+        return lib.eqat_distill_topk_strided(P(x), dt, ld, T, V, P(ids), P(FAKE), 4, 1.0, 0, None, P(loss), P(dx), ld_dx, None)
+
+    # all of these fail at dx, the others below only for want of a device
+    assert call(ld_dx=32) == SHAPE and call(ld_dx=1 << 31) == SHAPE
+    assert call(ld_dx=41) == SHAPE and call(ld_dx=44) == SHAPE and call(ld_dx=42, dt=0) == SHAPE
+    assert call(dx=FAKE, ld_dx=48) == SHAPE                   # x with another stride
+    good = [dict(ld_dx=48), dict(ld_dx=44, dt=0), dict(ld_dx=41, T=1), dict(dx=FAKE), dict(dx=FAKE, ld_dx=48, T=1),
+            dict(dx=FAKE + 2 * 40, ld=80, ld_dx=80), dict(x=FAKE + 2 * 40, dx=FAKE, ld=80, ld_dx=80),
+            dict(dx=FAKE + 3 * 80)]
+    if not torch.cuda.is_available():  # (they would run)
+        for kw in good:
+            assert call(**kw) not in (OK, SHAPE, UNSUP, ALIGN, NULL), kw
+    assert call(T=0) == OK and call(dx=0, ld_dx=0) == OK
+
+
 def test_fp4_refusals(lib):
     st = None
     pack = lambda x=FAKE, dt=1, N=3, K=64, fmt=1, g=FAKE, c=FAKE, s=FAKE: lib.eqat_pack_fp4(  # noqa: E731

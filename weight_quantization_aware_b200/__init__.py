@@ -70,6 +70,7 @@ def load_library():
         "eqat_adamw_step": [P, I, P, I, I64, P],
         "eqat_token_logprobs": [P, I, I64, I64, I64, P, ctypes.c_double, I, P, P, P, P, P],
         "eqat_distill_topk": [P, I, I64, I64, I64, P, P, I, ctypes.c_double, U32, P, P, P, P],
+        "eqat_distill_topk_strided": [P, I, I64, I64, I64, P, P, I, ctypes.c_double, U32, P, P, P, I64, P],
         "eqat_fp4_tensor_scale": [P, I, I64, P, P],
         "eqat_pack_fp4": [P, I, I64, I64, I, P, P, P, P],
         "eqat_fake_quant_fp4": [P, I, I64, I64, I, P, P, P],
@@ -583,22 +584,27 @@ def _distill(logits, ids, tlp, weight, temperature, tail, want_loss, want_grad, 
     k = ids.shape[1]
     ip, tp = _arg(ids, "ids", torch.int64, (T, k), dev), _arg(tlp, "tlp", torch.float32, (T, k), dev)
     wp = _opt(weight, "weight", torch.float32, (T,), dev)
-    gp = None
+    gp, ldg = None, ld
     if want_grad:
+        step = 16 // logits.element_size()  # rows of both start at the same place of 16 bytes
         if dlogits is None:
-            dlogits = logits.new_empty(T, ld)
-            dlogits = dlogits if ld == V else dlogits[:, :V]
+            # the strides of logits with a padded vocabulary; rows far apart come closer
+            ldg = ld if ld < 2 * V else V + (ld - V) % step
+            dlogits = logits.new_empty(T, ldg)
+            dlogits = dlogits if ldg == V else dlogits[:, :V]
         else:
             _shape(dlogits, "dlogits", (T, V))
-            if _rows(dlogits, "dlogits", dev)[2] != ld:
-                raise ValueError("dlogits must have the strides of logits")
+            ldg = _rows(dlogits, "dlogits", dev)[2]
+            if (ldg - ld) % step:
+                raise ValueError(f"dlogits must have a row stride that agrees with that of logits, {ld}, modulo {step}"
+                                 f" elements, got {ldg}")
             if dlogits.dtype != logits.dtype:
                 raise TypeError(f"dlogits must be {logits.dtype}, got {dlogits.dtype}")
         gp = dlogits.data_ptr()
     loss = tlp.new_empty(T) if want_loss else None
-    _check("eqat_distill_topk", lib.eqat_distill_topk(
+    _check("eqat_distill_topk", lib.eqat_distill_topk_strided(
         logits.data_ptr(), _dt(logits), ld, T, V, ip, tp, k, temperature, EQAT_DISTILL_TAIL if tail else 0, wp,
-        loss.data_ptr() if want_loss else None, gp, stream))
+        loss.data_ptr() if want_loss else None, gp, ldg, stream))
     return loss, dlogits
 
 
@@ -615,7 +621,8 @@ def distill_topk_fwd(logits, ids, tlp, weight=None, temperature=1.0, tail=False)
 def distill_topk_bwd(logits, ids, tlp, dloss, temperature=1.0, tail=False, dlogits=None):
     """Gradient of distill_topk_fwd's unweighted loss with respect to the logits, where
     dloss fp32 [T] arrives at it.  dlogits, if given, receives it and may be the logits
-    themselves (same strides)."""
+    themselves; its row stride agrees with theirs modulo 16 bytes.  A gradient made here has the logits' strides, or closer rows where
+    theirs are 2 V apart or more."""
     return _distill(logits, ids, tlp, dloss, temperature, tail, False, True, dlogits)[1]
 
 

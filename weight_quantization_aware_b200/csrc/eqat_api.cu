@@ -823,6 +823,16 @@ eqat_status check_rows(const void *x, int dt, int64_t ld, int64_t T, int64_t V, 
     return check_ptr(x, T * V, "x");
 }
 
+// dx beside x, elements of `es` bytes: rows that start at the same place of 16 bytes (both
+// bases are 16-byte aligned).
+eqat_status check_dx(const void *x, int64_t ld, const void *dx, int64_t ld_dx, int64_t T, int64_t V, int64_t es) {
+    if (ld_dx < V || ld_dx >= (int64_t(1) << 31)) return fail(EQAT_ERR_SHAPE, "the row stride of dx is out of range");
+    if (T > 1 && (ld_dx - ld) * es % 16 != 0)
+        return fail(EQAT_ERR_SHAPE, "the row strides of x and dx differ modulo 16 bytes");
+    if (T > 1 && x == dx && ld_dx != ld) return fail(EQAT_ERR_SHAPE, "x in place with another row stride");
+    return EQAT_OK;
+}
+
 // ------------------------------------------------------------------ microscaled 4-bit floats
 
 eqat_status check_fp4(int64_t M, int64_t N, int64_t K, int fmt, const float *gx, const float *gw) {
@@ -883,6 +893,13 @@ eqat_status eqat_token_logprobs(const void *x, int dt, int64_t ld, int64_t T, in
 eqat_status eqat_distill_topk(const void *x, int dt, int64_t ld, int64_t T, int64_t V, const int64_t *ids,
                               const float *tlp, int k, double temperature, uint32_t flags, const float *weight,
                               float *loss, void *dx, eqat_stream_t stream) {
+    return eqat_distill_topk_strided(x, dt, ld, T, V, ids, tlp, k, temperature, flags, weight, loss, dx, ld, stream);
+}
+
+eqat_status eqat_distill_topk_strided(const void *x, int dt, int64_t ld, int64_t T, int64_t V, const int64_t *ids,
+                                      const float *tlp, int k, double temperature, uint32_t flags,
+                                      const float *weight, float *loss, void *dx, int64_t ld_dx,
+                                      eqat_stream_t stream) {
     DeviceInfo dev;
     EQAT_TRY(check_rows(x, dt, ld, T, V, temperature));
     if (V > EQAT_DISTILL_MAX_V) return fail(EQAT_ERR_SHAPE, "V is above EQAT_DISTILL_MAX_V");
@@ -893,10 +910,11 @@ eqat_status eqat_distill_topk(const void *x, int dt, int64_t ld, int64_t T, int6
     EQAT_TRY(check_array(weight, 0, 4, "weight"));
     EQAT_TRY(check_array(loss, 0, 4, "loss"));
     EQAT_TRY(check_ptr(dx, 0, "dx"));
+    if (dx) EQAT_TRY(check_dx(x, ld, dx, ld_dx, T, V, dt == EQAT_F32 ? 4 : 2));
     if (T == 0 || (!loss && !dx)) return EQAT_OK;
     EQAT_TRY(get_device(dev));
     EQAT_CUDA(eqat::launch_distill_topk(x, dt == EQAT_F32, ld, T, V, ids, tlp, k, temperature,
-                                        (flags & EQAT_DISTILL_TAIL) != 0, weight, loss, dx, dev,
+                                        (flags & EQAT_DISTILL_TAIL) != 0, weight, loss, dx, ld_dx, dev,
                                         reinterpret_cast<cudaStream_t>(stream)),
               "distill_topk");
     return EQAT_OK;

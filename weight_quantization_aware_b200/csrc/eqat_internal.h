@@ -186,10 +186,11 @@ constexpr int64_t kDistillMaxV = int64_t(1) << 19;  // two bits per vocabulary e
 cudaError_t launch_token_logprobs(const void *x, bool f32, int64_t ld, int64_t T, int64_t V, const int64_t *targets,
                                   double temperature, int k, float *logprob, float *entropy, int64_t *top_ids,
                                   float *top_logprobs, const DeviceInfo &dev, cudaStream_t st);
-// dx (row stride ld, nullable) may be x; loss and weight are nullable.
+// dx (row stride ld_dx, which agrees with ld modulo 16 bytes; nullable) may be x; loss and
+// weight are nullable.
 cudaError_t launch_distill_topk(const void *x, bool f32, int64_t ld, int64_t T, int64_t V, const int64_t *ids,
                                 const float *tlp, int k, double temperature, bool tail, const float *weight,
-                                float *loss, void *dx, const DeviceInfo &dev, cudaStream_t st);
+                                float *loss, void *dx, int64_t ld_dx, const DeviceInfo &dev, cudaStream_t st);
 
 // ------------------------------------------------------------------ microscaled 4-bit floats
 // x [N, K] -> codes [N, K / 2] and scale tiles, or (codes and scales NULL) values [N, K];

@@ -958,7 +958,7 @@ __global__ void __launch_bounds__(W + 32, kLogprobCtas<TOP, W>) k_token_logprobs
 
 struct DistillArgs {
     const void *x;
-    int64_t ld, T, V;
+    int64_t ld, ld_dx, T, V;
     const int64_t *ids;
     const float *tlp;
     int k;
@@ -966,7 +966,7 @@ struct DistillArgs {
     double inv_tau;
     const float *weight;  // nullable: 1
     float *loss;          // nullable
-    void *dx;             // nullable; may be x
+    void *dx;             // nullable; may be x; its rows start as x's do, modulo 16 bytes
     int *err;
 };
 
@@ -1200,15 +1200,15 @@ __global__ void __launch_bounds__(W + 64, kCtasPerSm<W>) k_distill(const Distill
     pdl_wait();
     pdl_allow_dependents();
     RingPos pos;
-    auto row_of = [&](const void *x, int64_t t) {
-        return Row<T>(const_cast<T *>(static_cast<const T *>(x)) + t * a.ld, static_cast<int>(a.V));
+    auto row_of = [&](const void *x, int64_t ld, int64_t t) {
+        return Row<T>(const_cast<T *>(static_cast<const T *>(x)) + t * ld, static_cast<int>(a.V));
     };
     if (tid >= P) {
         if (tid == P) {
             for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
                 if (a.weight && a.weight[t] == 0.0f) continue;
-                ring_fill<W>(row_of(a.x, t), ring, ctl, pos, a.err, a.dx != nullptr);
-                if (a.dx) ring_fill<W>(row_of(a.x, t), ring, ctl, pos, a.err, false);
+                ring_fill<W>(row_of(a.x, a.ld, t), ring, ctl, pos, a.err, a.dx != nullptr);
+                if (a.dx) ring_fill<W>(row_of(a.x, a.ld, t), ring, ctl, pos, a.err, false);
             }
             ring_end(ctl);
         }
@@ -1230,8 +1230,8 @@ __global__ void __launch_bounds__(W + 64, kCtasPerSm<W>) k_distill(const Distill
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, turn ^= 1) {
         Slots &sl = slots[turn];
         uint32_t *bitmap = bitmaps + turn * words;
-        const Row<T> row = row_of(a.x, t);
-        const Row<T> out = row_of(a.dx ? a.dx : a.x, t);  // same phase as the row
+        const Row<T> row = row_of(a.x, a.ld, t);
+        const Row<T> out = a.dx ? row_of(a.dx, a.ld_dx, t) : row;  // same phase as the row
         const float w = sl.w;
         const bool skip = w == 0.0f;  // a token without a loss: nothing of its row is read
         if (walker && !skip) {
@@ -1424,8 +1424,8 @@ cudaError_t launch_token_logprobs(const void *x, bool f32, int64_t ld, int64_t T
 
 cudaError_t launch_distill_topk(const void *x, bool f32, int64_t ld, int64_t T, int64_t V, const int64_t *ids,
                                 const float *tlp, int k, double temperature, bool tail, const float *weight,
-                                float *loss, void *dx, const DeviceInfo &dev, cudaStream_t st) {
-    const DistillArgs a{x, ld, T, V, ids, tlp, k, static_cast<float>(1.44269504088896340736 / temperature),
+                                float *loss, void *dx, int64_t ld_dx, const DeviceInfo &dev, cudaStream_t st) {
+    const DistillArgs a{x, ld, ld_dx, T, V, ids, tlp, k, static_cast<float>(1.44269504088896340736 / temperature),
                         1.0 / temperature, weight, loss, dx, device_error_word()};
     if (!a.err) return cudaErrorInvalidSymbol;
     if (f32) return tail ? launch_distill_t<float, true>(a, dev, st) : launch_distill_t<float, false>(a, dev, st);
