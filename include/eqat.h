@@ -353,7 +353,8 @@ eqat_status eqat_token_logprobs(const void *x, int dt, int64_t ld, int64_t T, in
  *   loss[t] = weight[t] L                                   [T] fp32   (nullable)
  *   dx = weight[t] dL/dx, dtype dt, row stride ld           [T, V]     (nullable)
  * weight (nullable: all 1) is the token's weight, or the gradient that arrives at its
- * loss.  dx may be x itself.  A row of weight 0 is not read: loss 0, dx 0.  The same
+ * loss.  dx may be x itself, and does not overlap it otherwise.  A row of weight 0 is
+ * not read: loss 0, dx 0.  The same
  * holds, whatever its weight, for a row whose teacher has no mass (renormalised form)
  * and for one whose entries are all masked.  A masked entry under a slot with mass
  * gives a loss of +inf and a finite gradient.  An id given twice counts with its

@@ -372,7 +372,8 @@ def test_distill_gradient_of_rows_far_apart(dtype):
 
 
 def test_distill_gradient_beside_the_logits():
-    """Logits and gradient as two halves of one buffer's rows."""
+    """Logits and gradient as two halves of one buffer's rows; a gradient that overlaps its
+    logits is refused."""
     T, V = 40, 1000
     both = torch.randn(T, 2 * V, device="cuda")
     x, g = both[:, :V], both[:, V:]
@@ -382,6 +383,9 @@ def test_distill_gradient_beside_the_logits():
     keep = x.clone()
     eqat.distill_topk_bwd(x, ids, tlp, w, dlogits=g)
     assert torch.equal(g, want) and torch.equal(x, keep)
+    with pytest.raises(eqat.EqatError):
+        eqat.distill_topk_bwd(both[:-1, :V], ids[1:], tlp[1:], w[1:], dlogits=both[1:, :V])
+    assert torch.equal(x, keep)
 
 
 def test_distill_gradient_matches_differences():

@@ -151,14 +151,19 @@ def test_distill_refusals(lib):
 
 
 def test_distill_gradient_strides(lib):
-    """dx has a row stride of its own, which agrees with x's modulo 16 bytes."""
+    """dx has a row stride of its own, which agrees with x's modulo 16 bytes, and does not
+    overlap x unless it is x."""
     def call(x=FAKE, dx=FAKE + (1 << 20), ld=40, ld_dx=40, T=3, V=33, dt=1, loss=0, ids=FAKE):
         return lib.eqat_distill_topk_strided(P(x), dt, ld, T, V, P(ids), P(FAKE), 4, 1.0, 0, None, P(loss), P(dx), ld_dx, None)
 
     # all of these fail at dx, the others below only for want of a device
     assert call(ld_dx=32) == SHAPE and call(ld_dx=1 << 31) == SHAPE
     assert call(ld_dx=41) == SHAPE and call(ld_dx=44) == SHAPE and call(ld_dx=42, dt=0) == SHAPE
+    assert call(dx=FAKE + 16) == UNSUP                        # a few entries on
+    assert call(dx=FAKE + 80) == UNSUP                        # a row on
     assert call(dx=FAKE, ld_dx=48) == SHAPE                   # x with another stride
+    assert call(dx=FAKE + 2 * 40, ld=80, ld_dx=80, V=41) == UNSUP  # side by side, but not quite
+    assert call(x=FAKE + 2 * 40, dx=FAKE, ld=80, ld_dx=80, V=41) == UNSUP
     good = [dict(ld_dx=48), dict(ld_dx=44, dt=0), dict(ld_dx=41, T=1), dict(dx=FAKE), dict(dx=FAKE, ld_dx=48, T=1),
             dict(dx=FAKE + 2 * 40, ld=80, ld_dx=80), dict(x=FAKE + 2 * 40, dx=FAKE, ld=80, ld_dx=80),
             dict(dx=FAKE + 3 * 80)]

@@ -621,7 +621,8 @@ def distill_topk_fwd(logits, ids, tlp, weight=None, temperature=1.0, tail=False)
 def distill_topk_bwd(logits, ids, tlp, dloss, temperature=1.0, tail=False, dlogits=None):
     """Gradient of distill_topk_fwd's unweighted loss with respect to the logits, where
     dloss fp32 [T] arrives at it.  dlogits, if given, receives it and may be the logits
-    themselves; its row stride agrees with theirs modulo 16 bytes.  A gradient made here has the logits' strides, or closer rows where
+    themselves; otherwise it does not overlap them, and its row stride agrees with theirs
+    modulo 16 bytes.  A gradient made here has the logits' strides, or closer rows where
     theirs are 2 V apart or more."""
     return _distill(logits, ids, tlp, dloss, temperature, tail, False, True, dlogits)[1]
 

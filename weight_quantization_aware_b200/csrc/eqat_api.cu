@@ -824,13 +824,19 @@ eqat_status check_rows(const void *x, int dt, int64_t ld, int64_t T, int64_t V, 
 }
 
 // dx beside x, elements of `es` bytes: rows that start at the same place of 16 bytes (both
-// bases are 16-byte aligned).
+// bases are 16-byte aligned), and no entry of dx where another entry of x lies.
 eqat_status check_dx(const void *x, int64_t ld, const void *dx, int64_t ld_dx, int64_t T, int64_t V, int64_t es) {
     if (ld_dx < V || ld_dx >= (int64_t(1) << 31)) return fail(EQAT_ERR_SHAPE, "the row stride of dx is out of range");
     if (T > 1 && (ld_dx - ld) * es % 16 != 0)
         return fail(EQAT_ERR_SHAPE, "the row strides of x and dx differ modulo 16 bytes");
     if (T > 1 && x == dx && ld_dx != ld) return fail(EQAT_ERR_SHAPE, "x in place with another row stride");
-    return EQAT_OK;
+    if (T == 0 || x == dx) return EQAT_OK;
+    const int64_t a = static_cast<int64_t>(reinterpret_cast<uintptr_t>(x)) / es,
+                  b = static_cast<int64_t>(reinterpret_cast<uintptr_t>(dx)) / es;
+    if (b >= a + (T - 1) * ld + V || a >= b + (T - 1) * ld_dx + V) return EQAT_OK;
+    const int64_t off = ((b - a) % ld + ld) % ld;  // side by side in rows of one buffer
+    if (T > 1 && ld_dx == ld && off >= V && off + V <= ld) return EQAT_OK;
+    return fail(EQAT_ERR_UNSUPPORTED, "dx overlaps x without being x");
 }
 
 // ------------------------------------------------------------------ microscaled 4-bit floats
