@@ -354,12 +354,12 @@ eqat_status eqat_token_logprobs(const void *x, int dt, int64_t ld, int64_t T, in
  *   dx = weight[t] dL/dx, dtype dt, row stride ld           [T, V]     (nullable)
  * weight (nullable: all 1) is the token's weight, or the gradient that arrives at its
  * loss.  dx may be x itself, and does not overlap it otherwise.  A row of weight 0 is
- * not read: loss 0, dx 0.  The same
- * holds, whatever its weight, for a row whose teacher has no mass (renormalised form)
- * and for one whose entries are all masked.  A masked entry under a slot with mass
- * gives a loss of +inf and a finite gradient.  An id given twice counts with its
- * slots' masses together.  An id >= V, NaN or +inf in the row, or NaN or +inf in
- * tlp, makes the row's loss and gradient NaN.  V <= EQAT_DISTILL_MAX_V. */
+ * not read: loss 0, dx 0.  The same holds, whatever its weight, for a row whose teacher
+ * has no mass (renormalised form) and for one whose entries are all masked.  A masked
+ * entry under a slot with mass gives a loss of +inf and a finite gradient.  An id given
+ * twice counts with its slots' masses together.  The tlp of an empty slot is ignored,
+ * whatever it is.  An id >= V, NaN or +inf in the row, or NaN or +inf in the tlp of a
+ * slot that is not empty, makes the row's loss and gradient NaN.  V <= EQAT_DISTILL_MAX_V. */
 #define EQAT_DISTILL_TAIL 1u
 #define EQAT_DISTILL_MAX_V 524288
 eqat_status eqat_distill_topk(const void *x, int dt, int64_t ld, int64_t T, int64_t V, const int64_t *ids,

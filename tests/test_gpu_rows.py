@@ -285,6 +285,21 @@ def test_distill_edges(dtype, tail):
         check_distill(x, ids, tlp, w, 1.5, tail)
 
 
+@pytest.mark.parametrize("tail", [False, True], ids=["renorm", "tail"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_what_an_empty_slot_holds_is_ignored(dtype, tail):
+    inf, V = float("inf"), 2003
+    x = make(8, V, dtype, 6)
+    ids, tlp = teacher(x, 40, 9)
+    for t, v in enumerate([float("nan"), inf, -inf, 0.0, 1e30, 3e38, -3e38, float("nan")]):
+        ids[t, [3, 35]] = -1 - t
+        tlp[t, [3, 35]] = v
+    check_distill(x, ids, tlp, None, 1.0, tail)
+    ids[7] = -1
+    tlp[7] = float("nan")
+    check_distill(x, ids, tlp, None, 1.0, tail)
+
+
 def test_distill_tail_does_not_cancel():
     """Nearly all mass on the slots: the student's mass outside them is far below 2^-24."""
     V, k = 5000, 3

@@ -71,6 +71,18 @@ def test_distill_oracle_gradient_matches_differences(tail, tau):
     assert np.abs(grad.sum(1)).max() < 1e-12  # the loss does not change when a row is shifted
 
 
+@pytest.mark.parametrize("tail", [False, True])
+def test_distill_oracle_ignores_what_an_empty_slot_holds(tail):
+    rng = np.random.default_rng(8)
+    x, ids = rng.normal(size=(5, 30)), np.tile(np.arange(4), (5, 1))
+    tlp = np.log(rng.dirichlet(np.ones(5), size=5)[:, :4])
+    ids[:, 2] = -1
+    want = rows.distill_topk(x, np.delete(ids, 2, 1), np.delete(tlp, 2, 1), None, 1.0, tail)
+    tlp[:, 2] = [np.nan, np.inf, -np.inf, 0.0, 1e30]
+    for a, b in zip(rows.distill_topk(x, ids, tlp, None, 1.0, tail), want):
+        assert np.array_equal(a, b) and np.isfinite(a).all()
+
+
 def test_distill_oracle_is_zero_at_the_teacher():
     rng = np.random.default_rng(6)
     x = rng.normal(size=(3, 40))

@@ -610,7 +610,7 @@ def _distill(logits, ids, tlp, weight, temperature, tail, want_loss, want_grad, 
 
 def distill_topk_fwd(logits, ids, tlp, weight=None, temperature=1.0, tail=False):
     """Distillation loss [T] (fp32) of a student's logits [T, V] against a teacher's
-    alternatives: ids int64 [T, k] (negative: empty slot) and their log probabilities
+    alternatives: ids int64 [T, k] (negative: empty slot, its tlp is ignored) and their log probabilities
     tlp fp32 [T, k], as token_logprobs gives them.  tail=False renormalises the teacher
     over the slots; tail=True compares what it has outside them with the student's mass
     outside them.  weight fp32 [T] multiplies each row's loss; a row of weight 0 is
