@@ -75,3 +75,30 @@ def test_head_steps_of_many_then_few_tokens():
         want, want_dx = e2eqp.e2eqp_head_step(alone, X[:T], ids[:T], tlp[:T], cfg, 1)
         loss, dX = e2eqp.e2eqp_head_step(head, X[:T], ids[:T], tlp[:T], cfg, step)
         assert torch.equal(loss, want) and torch.equal(dX, want_dx)
+
+
+def test_head_step_without_tokens():
+    """A batch whose tokens are all masked away: no loss, dX of no rows, a gradient of 0 for
+    the scales (AdamW goes on by its moments)."""
+    V, K, k, bits, g = 136, 128, 4, 2, 64
+    d = synthetic.draw_linear(np.random.default_rng(9), 40, V, K, 0.1, "bf16")
+    X, W = d["X"].cuda(), d["W"].cuda()
+    s, z = eqat.minmax_init(W, bits, g)
+    codes, zq = eqat.pack_codes(W, s, z, bits, g)
+    teacher = (X.float() @ W.float().t()).to(torch.bfloat16)
+    ids, tlp = e2eqp.teacher_alternatives(teacher[:0], k)
+    assert ids.shape == (0, k) and tlp.shape == (0, k)
+    cfg = e2eqp.E2EQPConfig(bits=bits, group=g)
+    head = e2eqp.QuantHead(codes, zq, s.clone())
+    loss, dX = e2eqp.e2eqp_head_step(head, X[:0], ids, tlp, cfg, 1)
+    assert loss.shape == (0,) and dX.shape == (0, K)
+    assert torch.equal(head.s, s) and not head.moments[0].any() and not head.moments[1].any()
+    ids, tlp = e2eqp.teacher_alternatives(teacher, k)
+    e2eqp.e2eqp_head_step(head, X, ids, tlp, cfg, 2)
+    m, v, now = head.moments[0].clone(), head.moments[1].clone(), head.s.clone()
+    assert m.any()
+    e2eqp.e2eqp_head_step(head, X[:0], ids[:0], tlp[:0], cfg, 3)
+    # one fp32 rounding each of 0.9 m and 0.999 v, and of beta itself
+    assert torch.allclose(head.moments[0], 0.9 * m, rtol=2.0 ** -22, atol=0)
+    assert torch.allclose(head.moments[1], 0.999 * v, rtol=2.0 ** -22, atol=0)
+    assert not torch.equal(head.s, now)

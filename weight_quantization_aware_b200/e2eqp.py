@@ -59,14 +59,14 @@ def teacher_alternatives(logits, k, temperature=1.0):
 
 def e2eqp_head_step(head: QuantHead, X, ids, tlp, cfg: E2EQPConfig, step: int, weight=None):
     """One step (step >= 1): returns (loss fp32 [T], dX).  X [T, K] bf16; weight fp32 [T]
-    (default: 1 / T each, the mean over the tokens)."""
+    (default: 1 / T each, the mean over the tokens).  Without tokens the scales' gradient is 0."""
     T, K = X.shape
     N = head.codes.shape[0]
     need = load_library().eqat_workspace_bytes(T, N, K, cfg.bits, cfg.group, EQAT_BF16)
     if head.ws is None or head.ws.numel() < need:  # few tokens of a narrow layer need more than many
         head.ws = workspace(T, N, K, cfg.bits, cfg.group, X.dtype, X.device)
     if weight is None:
-        weight = torch.full((T,), 1.0 / T, dtype=torch.float32, device=X.device)
+        weight = torch.full((T,), 1.0 / max(T, 1), dtype=torch.float32, device=X.device)
     Y = dq_linear_fwd(X, head.codes, head.zq, head.s, cfg.bits, cfg.group, ws=head.ws)
     loss, dY = distill_topk_step(Y, ids, tlp, weight=weight, temperature=cfg.temperature, tail=cfg.tail, dlogits=Y)
     # a forward at decode sizes leaves no W-hat in the workspace
