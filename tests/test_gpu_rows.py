@@ -477,3 +477,23 @@ def test_rows_past_32_bit_offsets():
         assert abs(ent.item() - (np.log(S) - (2 * np.exp(2.0) + np.exp(1.0)) / S)) < 5e-5
     assert ids.tolist() == [[V - 1, V - 2, 0]]
     assert abs(top[0, 2].item() + np.log(S)) < 1e-5
+
+
+def test_refusals_on_the_device():
+    """Refused before anything of their size is allocated or launched."""
+    x, t = make(3, 40, torch.float32, 1), torch.zeros(3, dtype=torch.int64, device="cuda")
+    tlp = torch.zeros(3, 2, device="cuda")
+    for k in (129, -1, 1 << 40):
+        with pytest.raises(eqat.EqatError):
+            eqat.token_logprobs(x, t, top_k=k)
+    for call in [lambda: eqat.token_logprobs(x, None), lambda: eqat.token_logprobs(x, t.int()),
+                 lambda: eqat.token_logprobs(x.half(), t), lambda: eqat.distill_topk_fwd(x, None, tlp),
+                 lambda: eqat.distill_topk_fwd(x, t[:, None].expand(3, 2).contiguous(), None),
+                 lambda: eqat.distill_topk_bwd(x, t[:, None].expand(3, 2).contiguous(), tlp, t),
+                 lambda: eqat.distill_topk_step(x, t[:, None].expand(3, 2).contiguous(), tlp, dlogits=x.bfloat16())]:
+        with pytest.raises(TypeError):
+            call()
+    lp, ent, ids, top = eqat.token_logprobs(x[:0], t[:0], top_k=3)
+    assert lp.shape == ent.shape == (0,) and ids.shape == top.shape == (0, 3)
+    loss, grad = eqat.distill_topk_step(x[:0], ids, top)
+    assert loss.shape == (0,) and grad.shape == (0, 40)

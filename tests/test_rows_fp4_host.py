@@ -214,6 +214,29 @@ def test_fp4_refusals(lib):
     assert lib.eqat_fp4_workspace_bytes(3, 16, 64, 0, 1) == 16 * 64 * 2 + 512
 
 
+def test_binding_refuses_what_is_no_tensor():
+    x, t = torch.zeros(3, 40), torch.zeros(3, dtype=torch.int64)
+    tlp = torch.zeros(3, 2)
+    W, c = torch.zeros(8, 64, dtype=torch.bfloat16), torch.zeros(8, 32, dtype=torch.uint8)
+    s = torch.zeros(1, 1, 512, dtype=torch.uint8)
+    for call in [
+        lambda: eqat.token_logprobs(None, t),
+        lambda: eqat.token_logprobs([[0.0]], t),
+        lambda: eqat.distill_topk_fwd(None, t, tlp),
+        lambda: eqat.fp4_tensor_scale(None),
+        lambda: eqat.pack_fp4(None, "mx"),
+        lambda: eqat.fake_quant_fp4(W.tolist(), "mx"),
+        lambda: eqat.dequant_fp4(None, s, "mx"),
+        lambda: eqat.fp4_linear_fwd(None, c, s, "mx"),
+        lambda: eqat.fp4_linear_fwd(W, None, s, "mx"),
+        lambda: eqat.fp4_linear_bwd(W, c.tolist(), s, W, "mx"),
+    ]:
+        with pytest.raises(TypeError):
+            call()
+    with pytest.raises(ValueError):
+        eqat.fp4_scale_shape(8, 64, "fp8")
+
+
 def test_binding_refusals():
     x, t = torch.zeros(3, 40), torch.zeros(3, dtype=torch.int64)
     ids, tlp = torch.zeros(3, 2, dtype=torch.int64), torch.zeros(3, 2)

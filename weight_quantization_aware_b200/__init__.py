@@ -568,17 +568,21 @@ def token_logprobs(logits, targets, top_k=0, temperature=1.0):
     tp = _arg(targets, "targets", torch.int64, (T,), dev)
     lp, ent = torch.empty_like(targets, dtype=torch.float32), torch.empty_like(targets, dtype=torch.float32)
     ids = top = None
+    if not 0 <= top_k <= EQAT_TOP_MAX:
+        top_k = -1  # the library refuses it (a C int could not hold every other)
     if top_k > 0:
         ids, top = targets.new_empty(T, top_k), lp.new_empty(T, top_k)
     _check("eqat_token_logprobs", lib.eqat_token_logprobs(
         logits.data_ptr(), _dt(logits), ld, T, V, tp, temperature, top_k, lp.data_ptr(), ent.data_ptr(),
-        ids.data_ptr() if top_k > 0 else None, top.data_ptr() if top_k > 0 else None, stream))
+        None if ids is None else ids.data_ptr(), None if top is None else top.data_ptr(), stream))
     return lp, ent, ids, top
 
 
 def _distill(logits, ids, tlp, weight, temperature, tail, want_loss, want_grad, dlogits):
     lib, dev, stream = _enter()
     T, V, ld = _rows(logits, "logits", dev)
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids must be a torch.Tensor")
     if ids.dim() != 2:
         raise ValueError(f"ids must be 2-D [T, k], got shape {tuple(ids.shape)}")
     k = ids.shape[1]
@@ -647,6 +651,7 @@ def _fmt(fmt):
 
 def fp4_scale_shape(N: int, K: int, fmt: str):
     """Shape of the scale tiles of an [N, K] matrix: tiles of 128 rows by 4 blocks."""
+    _fmt(fmt)
     return (-(-N // 128), -(-(K // FP4_BLOCK[fmt]) // 4), 512)
 
 
@@ -661,6 +666,8 @@ def _fp4_matrix(W, name="W"):
 
 
 def _codes_matrix(codes):
+    if not isinstance(codes, torch.Tensor):
+        raise TypeError("codes must be a torch.Tensor")
     if codes.dim() != 2:
         raise ValueError(f"codes must be 2-D [N, K/2], got shape {tuple(codes.shape)}")
     return codes.shape[0], codes.shape[1] * 2
@@ -670,7 +677,8 @@ def fp4_tensor_scale(W, out=None):
     """The tensor scale of the "nv" format: the smallest power of two g with
     max|W| <= 6 * 448 * g, one fp32 value on the device."""
     lib, dev, stream = _enter()
-    wp = _arg(W, "W", W.dtype, _fp4_matrix(W), dev)
+    shape = _fp4_matrix(W)
+    wp = _arg(W, "W", W.dtype, shape, dev)
     out = W.new_empty(1, dtype=torch.float32) if out is None else out
     _check("eqat_fp4_tensor_scale", lib.eqat_fp4_tensor_scale(
         wp, _dt(W), W.numel(), _arg(out, "out", torch.float32, (1,), dev), stream))
@@ -722,6 +730,8 @@ def dequant_fp4(codes, scales, fmt, tscale=None, dtype=torch.bfloat16, out=None)
     gp = _opt(tscale, "tscale", torch.float32, (1,), dev)
     if out is None:
         out = codes.new_empty(N, K, dtype=dtype)
+    elif not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a torch.Tensor")
     op = _arg(out, "out", out.dtype, (N, K), dev)
     _check("eqat_dequant_fp4", lib.eqat_dequant_fp4(cp, sp, N, K, f, gp, op, _dt(out), stream))
     return out
