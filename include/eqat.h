@@ -420,7 +420,10 @@ eqat_status eqat_dequant_fp4(const uint8_t *codes, const uint8_t *scales, int64_
 
 /* Bytes of workspace of eqat_fp4_linear_fwd (backward == 0: X's codes and scales; 0 for
  * the few tokens, up to 16, whose X is packed inside the product) or
- * eqat_fp4_linear_bwd (the bf16 values of W and X); 0 for bad arguments. */
+ * eqat_fp4_linear_bwd (backward == 1: the bf16 values of W, for dX, and X, for dW;
+ * EQAT_FP4_ONLY_DX, EQAT_FP4_ONLY_DW: where the other gradient is NULL); 0 for bad arguments. */
+#define EQAT_FP4_ONLY_DX 2
+#define EQAT_FP4_ONLY_DW 3
 size_t eqat_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int backward);
 
 /* Y = X_hat W_hat^T with both operands in 4 bits: X [M, K] is packed in the call (with

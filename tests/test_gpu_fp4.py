@@ -284,6 +284,29 @@ def test_linear_bwd(case, fmt):
     assert none is None and torch.equal(only, dX)
 
 
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_backward_of_one_gradient(fmt):
+    """Each gradient alone, in a workspace of its own size and no byte more: the same bits as
+    together, and nothing written past the workspace."""
+    M, N, K = 301, 136, 544
+    X, W, dY = (draw(*s, torch.bfloat16, i, 1.0) for i, s in enumerate([(M, K), (N, K), (M, N)]))
+    X, dY = X.cuda(), dY.cuda()
+    g = scale_of(W, fmt)
+    codes, scales = packed(W, fmt, g)
+    want = eqat.fp4_linear_bwd(X, codes, scales, dY, fmt, tscale=g)
+    for dx, dw in ((True, False), (False, True), (True, True)):
+        n = eqat.fp4_workspace(M, N, K, fmt, backward=True, need_dx=dx, need_dw=dw).numel()
+        buf = torch.full((n + 4096,), 7, dtype=torch.uint8, device="cuda")
+        for ws in (None, buf[:n]):
+            got = eqat.fp4_linear_bwd(X, codes, scales, dY, fmt, tscale=g, need_dx=dx, need_dw=dw, ws=ws)
+            for a, b, need in zip(got, want, (dx, dw)):
+                assert torch.equal(a, b) if need else a is None
+        assert bool((buf[n:] == 7).all())
+        with pytest.raises(eqat.EqatError):
+            eqat.fp4_linear_bwd(X, codes, scales, dY, fmt, tscale=g, need_dx=dx, need_dw=dw, ws=buf[:n - 1])
+    assert eqat.fp4_linear_bwd(X, codes, scales, dY, fmt, tscale=g, need_dx=False, need_dw=False) == (None, None)
+
+
 def test_backward_matches_differences():
     """The product is linear in each packed operand: dX against the change of sum(dY Y)
     when a block of X moves along the packed grid by whole codes (both exact)."""

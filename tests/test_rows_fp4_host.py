@@ -214,6 +214,19 @@ def test_fp4_refusals(lib):
     assert lib.eqat_fp4_workspace_bytes(3, 16, 64, 0, 1) == 16 * 64 * 2 + 512
 
 
+def test_fp4_backward_workspace_of_one_gradient(lib):
+    """Only the values that a gradient takes have to fit."""
+    M, N, K = 300, 24, 64
+    w, x = N * K * 2, M * K * 2
+    q = lambda b: lib.eqat_fp4_workspace_bytes(M, N, K, 1, b)  # noqa: E731
+    assert (q(1), q(2), q(3)) == (w + x, w, x)
+    bwd = lambda dX, dW, n: lib.eqat_fp4_linear_bwd(  # noqa: E731
+        P(FAKE), P(FAKE), P(FAKE), 1, P(0), P(0), P(FAKE), P(dX), P(dW), M, N, K, P(FAKE), n, None)
+    assert bwd(FAKE, 0, w - 1) == WS and bwd(0, FAKE, x - 1) == WS and bwd(FAKE, FAKE, w + x - 1) == WS
+    if not torch.cuda.is_available():  # (they would run)
+        assert WS not in (bwd(FAKE, 0, w), bwd(0, FAKE, x), bwd(FAKE, FAKE, w + x))
+
+
 def test_binding_refuses_what_is_no_tensor():
     x, t = torch.zeros(3, 40), torch.zeros(3, dtype=torch.int64)
     tlp = torch.zeros(3, 2)

@@ -737,9 +737,16 @@ def dequant_fp4(codes, scales, fmt, tscale=None, dtype=torch.bfloat16, out=None)
     return out
 
 
-def fp4_workspace(M, N, K, fmt, backward=False, device=None) -> torch.Tensor:
-    """A uint8 CUDA buffer for fp4_linear_fwd (or, with backward, fp4_linear_bwd)."""
-    n = int(load_library().eqat_fp4_workspace_bytes(M, N, K, _fmt(fmt), int(backward)))
+def _fp4_backward(need_dx, need_dw):
+    """eqat_fp4_workspace_bytes's word for the gradients that are wanted."""
+    return 1 if need_dx == need_dw else 2 if need_dx else 3
+
+
+def fp4_workspace(M, N, K, fmt, backward=False, device=None, need_dx=True, need_dw=True) -> torch.Tensor:
+    """A uint8 CUDA buffer for fp4_linear_fwd (or, with backward, fp4_linear_bwd of the
+    gradients that are needed)."""
+    n = int(load_library().eqat_fp4_workspace_bytes(M, N, K, _fmt(fmt),
+                                                    _fp4_backward(need_dx, need_dw) if backward else 0))
     return torch.empty(max(n, 1), dtype=torch.uint8, device=device or "cuda")
 
 
@@ -773,7 +780,7 @@ def fp4_linear_fwd(X, codes, scales, fmt, tscale=None, x_tscale=None, ws=None, Y
         yp = Y.data_ptr()
     else:
         yp = _arg(Y, "Y", torch.bfloat16, (M, N), dev)
-    ws, wp, wn = _fp4_ws(ws, M, N, K, fmt, False, dev, codes)
+    ws, wp, wn = _fp4_ws(ws, M, N, K, fmt, 0, dev, codes)
     _check("eqat_fp4_linear_fwd", lib.eqat_fp4_linear_fwd(xp, cp, sp, f, gx, gw, yp, M, N, K, wp, wn, stream))
     return Y
 
@@ -791,7 +798,9 @@ def fp4_linear_bwd(X, codes, scales, dY, fmt, tscale=None, x_tscale=None, need_d
         dW = X.new_empty(N, K) if need_dw else None
     else:
         dX, dW = out
-    ws, wp, wn = _fp4_ws(ws, M, N, K, fmt, True, dev, codes)
+    if dX is None and dW is None:
+        return dX, dW
+    ws, wp, wn = _fp4_ws(ws, M, N, K, fmt, _fp4_backward(dX is not None, dW is not None), dev, codes)
     _check("eqat_fp4_linear_bwd", lib.eqat_fp4_linear_bwd(
         xp, cp, sp, f, gx, gw, dyp, _opt(dX, "dX", torch.bfloat16, (M, K), dev),
         _opt(dW, "dW", torch.bfloat16, (N, K), dev), M, N, K, wp, wn, stream))

@@ -860,11 +860,14 @@ int64_t fp4_scale_bytes(int64_t N, int64_t K, int fmt) {
 
 size_t up256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
-size_t fp4_ws(int64_t M, int64_t N, int64_t K, int fmt, bool backward) {
-    const size_t m = static_cast<size_t>(M), n = static_cast<size_t>(N), k = static_cast<size_t>(K);
-    if (backward) return up256(n * k * 2) + up256(m * k * 2);
+size_t fp4_fwd_ws(int64_t M, int64_t N, int64_t K, int fmt) {
     if (eqat::fp4_packs_in_product(M, N, K)) return 0;
-    return up256(m * k / 2) + static_cast<size_t>(fp4_scale_bytes(M, K, fmt));
+    return up256(static_cast<size_t>(M * K) / 2) + static_cast<size_t>(fp4_scale_bytes(M, K, fmt));
+}
+
+// dX takes the bf16 values of W, dW those of X.
+size_t fp4_bwd_ws(int64_t M, int64_t N, int64_t K, bool dx, bool dw) {
+    return (dx ? up256(static_cast<size_t>(N * K) * 2) : 0) + (dw ? up256(static_cast<size_t>(M * K) * 2) : 0);
 }
 
 eqat_status check_fp4_ws(const void *ws, size_t ws_bytes, size_t need) {
@@ -933,7 +936,8 @@ size_t eqat_fp4_scale_bytes(int64_t N, int64_t K, int fmt) {
 
 size_t eqat_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int fmt, int backward) {
     if (check_fp4(M, N, K, fmt, nullptr, nullptr) != EQAT_OK) return 0;
-    return fp4_ws(M, N, K, fmt, backward != 0);
+    if (backward == 0) return fp4_fwd_ws(M, N, K, fmt);
+    return fp4_bwd_ws(M, N, K, backward != EQAT_FP4_ONLY_DW, backward != EQAT_FP4_ONLY_DX);
 }
 
 eqat_status eqat_fp4_tensor_scale(const void *x, int dt, int64_t n, float *g, eqat_stream_t stream) {
@@ -1006,7 +1010,7 @@ eqat_status eqat_fp4_linear_fwd(const void *X, const uint8_t *codes, const uint8
     EQAT_TRY(check_ptr(scales, N * K, "scales"));
     EQAT_TRY(check_ptr(Y, M * N, "Y"));
     if (M * N == 0) return EQAT_OK;
-    if (K > 0) EQAT_TRY(check_fp4_ws(ws, ws_bytes, fp4_ws(M, N, K, fmt, false)));
+    if (K > 0) EQAT_TRY(check_fp4_ws(ws, ws_bytes, fp4_fwd_ws(M, N, K, fmt)));
     EQAT_TRY(get_device(dev));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (K == 0) {
@@ -1037,7 +1041,7 @@ eqat_status eqat_fp4_linear_bwd(const void *X, const uint8_t *codes, const uint8
     EQAT_TRY(check_ptr(dX, 0, "dX"));
     EQAT_TRY(check_ptr(dW, 0, "dW"));
     if ((!dX && !dW) || K == 0) return EQAT_OK;
-    if (M * N > 0) EQAT_TRY(check_fp4_ws(ws, ws_bytes, fp4_ws(M, N, K, fmt, true)));
+    if (M * N > 0) EQAT_TRY(check_fp4_ws(ws, ws_bytes, fp4_bwd_ws(M, N, K, dX != nullptr, dW != nullptr)));
     EQAT_TRY(get_device(dev));
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (M * N == 0) {  // empty sums
@@ -1046,7 +1050,7 @@ eqat_status eqat_fp4_linear_bwd(const void *X, const uint8_t *codes, const uint8
         return EQAT_OK;
     }
     const bool nv = fmt == EQAT_FP4_NV;
-    uint8_t *w_hat = static_cast<uint8_t *>(ws), *x_hat = w_hat + up256(static_cast<size_t>(N * K) * 2);
+    uint8_t *w_hat = static_cast<uint8_t *>(ws), *x_hat = w_hat + fp4_bwd_ws(M, N, K, dX != nullptr, false);
     // both contractions in one grouped launch: the tiles of one fill the last wave of the other
     eqat::GemmProblem probs[2];
     int np = 0;
