@@ -436,7 +436,8 @@ eqat_status eqat_fp4_linear_fwd(const void *X, const uint8_t *codes, const uint8
 
 /* The straight-through backward of eqat_fp4_linear_fwd (packing has an identity
  * gradient):  dX = dY W_hat  [M, K],  dW = dY^T X_hat  [N, K], both bf16 and nullable,
- * with the bf16 values of the packed operands. */
+ * with the bf16 values of the packed operands: those of the forward where the tensor
+ * scale is a power of two, and otherwise within 2^-8 of them. */
 eqat_status eqat_fp4_linear_bwd(const void *X, const uint8_t *codes, const uint8_t *scales, int fmt,
                                 const float *gx, const float *gw, const void *dY, void *dX, void *dW, int64_t M,
                                 int64_t N, int64_t K, void *ws, size_t ws_bytes, eqat_stream_t stream);

@@ -284,6 +284,31 @@ def test_linear_bwd(case, fmt):
     assert none is None and torch.equal(only, dX)
 
 
+@pytest.mark.parametrize("M", [3, 16, 40, 128, 300])
+def test_product_with_any_tensor_scale(M):
+    """Tensor scales that are no power of two (amax / 2688, as other packers write): the
+    forward multiplies exact codes and scales, and the fp32 sum by both tensor scales (two
+    roundings; the oracle rounds each block's scale times g, two more: 4 2^-24 in all).  The
+    backward's values are those rounded to bf16."""
+    N, K = 264, 1184
+    X, W, dY = draw(M, K, torch.bfloat16, 1, 1.0), draw(N, K, torch.bfloat16, 2), draw(M, N, torch.bfloat16, 3, 0.01)
+    gx, gw = ((t.float().abs().max() / 2688).reshape(1).cuda() for t in (X, W))
+    codes, scales = packed(W, "nv", gw)
+    Y = eqat.fp4_linear_fwd(X.cuda(), codes, scales, "nv", tscale=gw, x_tscale=gx)
+    xv, wv = values(X, "nv", gx), values(W, "nv", gw)
+    ref, mag = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    bound = 2.0 ** -8 * np.abs(ref) + (K / 64 + 9) * 2.0 ** -22 * mag
+    assert (np.abs(f32(Y) - ref) <= bound).all()
+    dX, dW = eqat.fp4_linear_bwd(X.cuda(), codes, scales, dY.cuda(), "nv", tscale=gw, x_tscale=gx)
+    xb, wb = (f32(torch.from_numpy(v.astype(np.float32)).to(torch.bfloat16)).astype(np.float64) for v in (xv, wv))
+    assert not np.array_equal(xb, xv) and (np.abs(wb - wv) <= 2.0 ** -8 * np.abs(wv)).all()
+    dy = f32(dY).astype(np.float64)
+    for got, a, b, n in ((dX, dy, wb, N), (dW, dy.T, xb, M)):
+        ref, mag = a @ b, np.abs(a) @ np.abs(b)
+        bound = 2.0 ** -8 * np.abs(ref) + (n / 16 + 8) * 2.0 ** -22 * mag + 1e-37
+        assert (np.abs(f32(got) - ref) <= bound).all()
+
+
 @pytest.mark.parametrize("fmt", ["mx", "nv"])
 def test_backward_of_one_gradient(fmt):
     """Each gradient alone, in a workspace of its own size and no byte more: the same bits as

@@ -788,7 +788,10 @@ def fp4_linear_fwd(X, codes, scales, fmt, tscale=None, x_tscale=None, ws=None, Y
 def fp4_linear_bwd(X, codes, scales, dY, fmt, tscale=None, x_tscale=None, need_dx=True, need_dw=True, ws=None,
                    out=None):
     """Straight-through backward of fp4_linear_fwd: returns (dX = dY W_hat,
-    dW = dY^T X_hat), None where not requested."""
+    dW = dY^T X_hat), None where not requested.  W_hat and X_hat are the bf16 values of the
+    packed operands: exact where the tensor scale is a power of two (as fp4_tensor_scale
+    gives); with another one they are rounded, by 2^-8 of themselves at most, while the
+    forward multiplies the packed values themselves."""
     f = _fmt(fmt)
     lib, dev, stream = _enter()
     M, N, K, xp, cp, sp, gw, gx = _fp4_operands(X, codes, scales, fmt, tscale, x_tscale, dev)
