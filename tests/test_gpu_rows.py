@@ -497,3 +497,23 @@ def test_refusals_on_the_device():
     assert lp.shape == ent.shape == (0,) and ids.shape == top.shape == (0, 3)
     loss, grad = eqat.distill_topk_step(x[:0], ids, top)
     assert loss.shape == (0,) and grad.shape == (0, 40)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_distill_at_the_limits_of_v(dtype):
+    """The largest vocabulary, and both sides of the largest one whose slots' bits fit beside
+    the wide ring (few long rows); slots at both ends of a row."""
+    for V in (524288, 262136, 262137, 262140, 262141):
+        x = make(2, V, dtype, V)
+        ids, tlp = teacher(x, 6, 1)
+        ids[1, 0], ids[1, 1], ids[1, 2] = V - 1, 0, V - 9
+        x[1, torch.tensor([0, V - 9, V - 1])] += 9.0
+        w = torch.tensor([1.0, 0.5], device="cuda")
+        for tail in (False, True):
+            check_distill(x, ids, tlp, w, 1.0, tail)
+        # rows of another phase: none starts on 16 bytes but the first
+        wide = torch.full((2, V + 3), float("nan"), dtype=dtype, device="cuda")
+        wide[:, :V] = x
+        check_distill(wide[:, :V], ids, tlp, w, 1.0, True)
+    with pytest.raises(eqat.EqatError):
+        eqat.distill_topk_fwd(make(1, 524289, dtype, 1), ids[:1], tlp[:1])
