@@ -473,3 +473,63 @@ def test_calls_at_once_on_three_streams():
     torch.cuda.synchronize()
     for j, t in got:
         assert torch.equal(t, want[j])
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+@pytest.mark.parametrize("M,N,K", [(17, 8, 32), (40, 136, 32), (64, 8, 96), (100, 1000, 32), (128, 8, 4064), (129, 8, 32)])
+def test_products_of_short_sides(M, N, K, fmt):
+    check_product(M, N, K, fmt, repeats=2)
+
+
+@pytest.mark.parametrize("fmt", ["mx", "nv"])
+def test_product_past_32_bit_offsets_of_y(fmt):
+    """More than 2^31 products: the last rows and columns are what their operands give alone
+    (one stage of K, the same sums in either call), and the backward of the last rows."""
+    M, N, K = 40968, 60008, 64
+    X, W = draw(M, K, torch.bfloat16, 1, 1.0).cuda(), draw(N, K, torch.bfloat16, 2).cuda()
+    gx, gw = scale_of(X, fmt), scale_of(W, fmt)
+    codes, scales = eqat.pack_fp4(W, fmt, tscale=gw)
+    Y = eqat.fp4_linear_fwd(X, codes, scales, fmt, tscale=gw, x_tscale=gx)
+    assert Y.numel() > 1 << 31
+    want = eqat.fp4_linear_fwd(X[-300:], codes, scales, fmt, tscale=gw, x_tscale=gx)
+    assert torch.equal(Y[-300:], want)
+    c, s = eqat.pack_fp4(W[-264:], fmt, tscale=gw)
+    assert torch.equal(Y[:, -264:], eqat.fp4_linear_fwd(X, c, s, fmt, tscale=gw, x_tscale=gx))
+    dX, _ = eqat.fp4_linear_bwd(X, codes, scales, Y, fmt, tscale=gw, x_tscale=gx, need_dw=False)
+    dy, wv = Y[-300:].double(), torch.from_numpy(values(W, fmt, gw)).cuda()
+    ref, mag = dy @ wv, dy.abs() @ wv.abs()
+    bound = 2.0 ** -8 * ref.abs() + (N / 16 + 8) * 2.0 ** -22 * mag
+    assert bool(((dX[-300:].double() - ref).abs() <= bound).all())
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose very first calls are captured: nothing of a kernel's preparation may
+    need the stream."""
+    import subprocess
+    import sys
+    code = """
+import torch, weight_quantization_aware_b200 as eqat
+x = torch.randn(300, 1000, device="cuda", dtype=torch.bfloat16)
+X, W = x[:40, :64].contiguous(), x[:264, :64].contiguous()
+XL = x[:, :64].contiguous()
+t = torch.arange(300, device="cuda")
+def run():
+    out = list(eqat.token_logprobs(x, t, top_k=5))
+    out += eqat.distill_topk_step(x, out[2], out[3], tail=True)
+    g = eqat.fp4_tensor_scale(W)
+    c, s = eqat.pack_fp4(W, "nv", tscale=g)
+    for a in (X[:2], X, XL):
+        y = eqat.fp4_linear_fwd(a, c, s, "nv", tscale=g)
+        out += [y, *eqat.fp4_linear_bwd(a, c, s, y, "nv", tscale=g)]
+    return out
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+for a, b in zip(got, run()):
+    assert torch.equal(a, b)
+assert eqat.device_error() == 0
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

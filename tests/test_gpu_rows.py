@@ -207,7 +207,7 @@ def test_top_k_of_uneven_and_tied_rows(dtype):
         check_logprobs(y, torch.arange(len(y), device="cuda"), k)
 
 
-def check_distill(x, ids, tlp, w, tau, tail):
+def check_distill(x, ids, tlp, w, tau, tail, least=1e-37):
     V = x.shape[1]
     want_l, want_g = orc.distill_topk(f64(x), ids.cpu().numpy(), f64(tlp), None if w is None else f64(w), tau, tail)
     loss, grad = eqat.distill_topk_step(x, ids, tlp, weight=w, temperature=tau, tail=tail)
@@ -223,7 +223,7 @@ def check_distill(x, ids, tlp, w, tau, tail):
         p = np.nan_to_num(np.exp(z) / np.exp(z).sum(1, keepdims=True))
     mag = 2 * p + np.abs(np.nan_to_num(want_g)) / np.maximum(wn[:, None], 1e-30) * tau
     rel = e + 2.0 ** -20 + 150 * 2.0 ** -23
-    bound = wn[:, None] / tau * mag * rel + np.abs(np.nan_to_num(want_g)) * (HALF[x.dtype] + 2.0 ** -22) + 1e-37
+    bound = wn[:, None] / tau * mag * rel + np.abs(np.nan_to_num(want_g)) * (HALF[x.dtype] + 2.0 ** -22) + least
     same(f64(grad), want_g, bound, "gradient")
     # the separate calls give the same bits
     assert torch.equal(eqat.distill_topk_fwd(x, ids, tlp, weight=w, temperature=tau, tail=tail).nan_to_num(7.0), loss.nan_to_num(7.0))
@@ -517,3 +517,37 @@ def test_distill_at_the_limits_of_v(dtype):
         check_distill(wide[:, :V], ids, tlp, w, 1.0, True)
     with pytest.raises(eqat.EqatError):
         eqat.distill_topk_fwd(make(1, 524289, dtype, 1), ids[:1], tlp[:1])
+
+
+@pytest.mark.parametrize("tau", [1e-6, 0.05, 30.0, 1e6])
+def test_distill_temperatures(tau):
+    """2^y below 2^-126 is 0 (ex2 flushes it), before it is multiplied by 1 / (tau S) or, outside
+    the slots, by at most that and as much again for the teacher's rest (S >= 1, the largest
+    entry's term): a gradient is off by up to 2^-125 / tau for that alone, more than 1e-37
+    where tau is small."""
+    x = make(6, 4097, torch.float32, 1)
+    ids, tlp = teacher(x, 20, 3, tau)
+    for tail in (False, True):
+        check_distill(x, ids, tlp, None, tau, tail, least=1e-37 + 2.0 ** -125 / tau)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("V", [1, 2, 3, 5, 7, 9])
+def test_many_rows_within_a_vector(V, dtype):
+    """Rows that share their 16 bytes with their neighbours, which other blocks take: the
+    gradient in place, the columns past V as they were."""
+    T, k = 3000, min(V, 3)
+    for ld in (V, V + 1):
+        x = make(T, V, dtype, V, ld)
+        t = torch.arange(T, device="cuda") % V
+        check_logprobs(x, t, k)
+        check_logprobs(x, t, 0)
+        ids, tlp = teacher(x, k, 5)
+        w = torch.rand(T, device="cuda")
+        w[::7] = 0.0
+        for tail in (False, True):
+            _, want = check_distill(x, ids, tlp, w, 1.0, tail)
+            buf = torch.full((T, ld), 3.0, dtype=dtype, device="cuda")
+            buf[:, :V] = x
+            eqat.distill_topk_bwd(buf[:, :V], ids, tlp, w, tail=tail, dlogits=buf[:, :V])
+            assert torch.equal(buf[:, :V], want) and bool((buf[:, V:] == 3.0).all())
