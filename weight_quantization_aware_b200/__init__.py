@@ -559,7 +559,7 @@ def _rows(x, name, dev):
 
 def token_logprobs(logits, targets, top_k=0, temperature=1.0):
     """Log probabilities of `targets` (int64 [T]; negative: not scored) under the rows of
-    logits [T, V] (bf16 or fp32, rows may be strided), with each row's entropy and top
+    logits [T, V] (bf16 or fp32, the first row on 16 bytes, rows may be strided), with each row's entropy and top
     alternatives: returns (logprob [T], entropy [T], top_ids int64 [T, top_k],
     top_logprobs [T, top_k]), fp32 except the ids; the last two are None where top_k is
     0.  Equal logits rank by index; alternatives that a row lacks have id -1."""

@@ -5,8 +5,10 @@
 // of bf16), a warp 512 consecutive values of a row, the next of which are on their way
 // while one is encoded.  Measured on 28672 x 8192 bf16 (a copy runs at 6.55 TB/s): tensor
 // scale 75 us (6.3 TB/s), pack mx 100 us (5.9) and nv 136 us (4.4), fake quantization mx 164
-// and nv 168 us (5.7, 5.6), values from codes 111 us (5.4).  nv packing is bound by
-// instruction issue: the exact division by the block's scale.
+// and nv 168 us (5.7, 5.6), values from codes 111 us (5.4).  nv packing is bound by its
+// instructions, those of the exact division by the block's scale and those that put signs
+// back: 67% of the cycles issue, the integer and logic pipe is 62% busy, and of 8 cycles that a
+// warp spends on an instruction 0.8 wait for memory (mx: 63%, 66%, 5.3 of 11.7).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

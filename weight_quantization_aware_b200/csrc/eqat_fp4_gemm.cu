@@ -8,7 +8,10 @@
 // (k_gemm2_fp4), whose 256 x 256 tiles reuse what they read.  Measured with the packing of
 // X (nv, graph replays): 1 token of 11008 x 4096 7.7 us (3.3 TB/s of packed weights), 64 tokens
 // 11.9 us, 128 tokens 13.1 us, 1 token of 28672 x 8192 27 us (4.9 TB/s); 4096 tokens of 11008 x 4096
-// 91 us (4.05 PFLOP/s), 8192^3 236 us (4.65; mx 214 us, 5.15).
+// 91 us (4.05 PFLOP/s), 8192^3 236 us (4.65; mx 214 us, 5.15).  The large ones are of a few
+// dozen calls, during which the SM clock stays at 1965 MHz; when calls on random data go on
+// for tens of milliseconds the power cap takes it to 1650 MHz, and the 4096 tokens take 105 us
+// (mx 84 and 97).
 //
 // k_gemm_fp4: a CTA makes one 128 x NT tile of W X^T.  A producer thread brings stages of 256 K values: the
 // code tiles by TMA (128 bytes of K per row, 128-byte swizzle) and the scale tiles by
@@ -699,7 +702,7 @@ constexpr int kDecThreads = 256;    // producer, issuer (after packing), packers
 constexpr int kDecMaxSlice = 2048;  // K values of a CTA
 constexpr int kDecStages = 4;
 constexpr int kDecTmem = 256;       // two CTAs share an SM's 512 columns
-constexpr int kDecSms = 148;
+constexpr int kDecSms = 148;        // of a B200; the workspace's size, which follows, is asked for without a device
 
 template <bool NV>
 struct DecCfg {

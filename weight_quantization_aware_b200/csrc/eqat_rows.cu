@@ -14,13 +14,16 @@
 // whose S is not finite (a NaN, an infinity) is walked again with x - m formed first.  The
 // second walk (top alternatives, gradient) reads the row again while it is in L2.
 //
-// What bounds the first walk besides memory is ex2 (a quarter of the issue rate), then
-// instruction issue: one packed-fp32 instruction does two entries of each step.
+// No one unit bounds the first walk: of 2048 x 32000 bf16, ex2 (a quarter of the issue
+// rate) is busy half of the time, instructions issue in 61% of the cycles (one packed-fp32
+// instruction does two entries of each step), DRAM runs at 47%, and the rest is the latency of
+// loads and a last round of rows that is less than half full.
 //
-// Measured, bf16 (a copy runs at 6.55 TB/s): log probabilities of 2048 x 32000 29.5 us (4.4
-// TB/s) and of 1024 x 131072 49.8 us (5.4 TB/s), with 64 alternatives 67 and 84 us; the
-// distillation step of 2048 x 32000 with 64 slots 71 us (3.7 TB/s; the block meets at
-// two barriers between a row's walks) and the gradient alone of 2048 x 131072 214 us (5.0 TB/s).
+// Measured, bf16, calls back to back (a copy runs at 6.55 TB/s): log probabilities of
+// 2048 x 32000 29-30 us (4.4 TB/s; fp32 45 us, 5.8 TB/s) and of 1024 x 131072 50 us (5.4
+// TB/s), with 64 alternatives 66-68 and 84 us; the distillation step of 2048 x 32000 with
+// 64 slots 70-71 us (3.7 TB/s; the block meets at two barriers between a row's walks), its loss
+// alone 41 us, and the gradient alone of 2048 x 131072 211-226 us from box to box (4.8-5.1 TB/s).
 //
 // All sums are fp32 per thread (a few hundred terms of one sign), joined over the
 // block in a fixed order; the few values per row (log S, the loss) are fp64.
@@ -1393,8 +1396,8 @@ cudaError_t launch_distill_w(const DistillArgs &a, const DeviceInfo &dev, cudaSt
     cudaError_t e = allow_smem(kern, kRingBytes<W> + most, done, dev);
     if (e != cudaSuccess) return e;
     // The rows that are walked twice at a time have to stay in the 126 MB L2 beside what
-    // is written: 2048 rows of 131072 bf16 take 207 us with two blocks per SM, 240 us with
-    // three and 278 us with one.
+    // is written: 2048 rows of 131072 bf16 take 222 us with two blocks per SM, 258 us with
+    // three and 296 us with one (in one run, on one box).
     const int64_t row_bytes = a.V * static_cast<int64_t>(sizeof(T)) * dev.sm_count;
     const int64_t per_sm =
         std::max<int64_t>(1, std::min<int64_t>(kCtasPerSm<W>, (80ll << 20) / std::max<int64_t>(row_bytes, 1)));
