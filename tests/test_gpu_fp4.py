@@ -284,6 +284,26 @@ def test_linear_bwd(case, fmt):
     assert none is None and torch.equal(only, dX)
 
 
+@pytest.mark.parametrize("M,N,K", [(4100, 264, 2080), (264, 8200, 2080), (3000, 3000, 544), (2060, 136, 8224), (70, 5128, 4128)])
+def test_backward_of_uneven_contractions(M, N, K):
+    """Both contractions in one launch, one of them several times as deep as the other (their
+    tiles are dealt by cost), or with several tiles per pair; ragged in every size."""
+    fmt = "nv"
+    X, W, dY = draw(M, K, torch.bfloat16, 1, 1.0), draw(N, K, torch.bfloat16, 2), draw(M, N, torch.bfloat16, 3, 0.01).cuda()
+    gx, gw = scale_of(X, fmt), scale_of(W, fmt)
+    codes, scales = packed(W, fmt, gw)
+    X = X.cuda()
+    dX, dW = eqat.fp4_linear_bwd(X, codes, scales, dY, fmt, tscale=gw, x_tscale=gx)
+    xv, wv = (torch.from_numpy(values(t, fmt, g)).cuda() for t, g in ((X, gx), (W, gw)))
+    dy = dY.double()
+    for got, a, b, n in ((dX, dy, wv, N), (dW, dy.t(), xv, M)):
+        ref, mag = a @ b, a.abs() @ b.abs()
+        bound = 2.0 ** -8 * ref.abs() + (n / 16 + 8) * 2.0 ** -22 * mag + 1e-37
+        assert bool(((got.double() - ref).abs() <= bound).all())
+    again = eqat.fp4_linear_bwd(X, codes, scales, dY, fmt, tscale=gw, x_tscale=gx)
+    assert torch.equal(again[0], dX) and torch.equal(again[1], dW)
+
+
 @pytest.mark.parametrize("M", [3, 16, 40, 128, 300])
 def test_product_with_any_tensor_scale(M):
     """Tensor scales that are no power of two (amax / 2688, as other packers write): the
