@@ -28,11 +28,10 @@
 #include <atomic>
 #include <cstdint>
 #include <cstdlib>
+#include <functional>
 #include <mutex>
-#include <queue>
 #include <type_traits>
 #include <utility>
-#include <vector>
 
 #include "eqat_internal.h"
 #include "eqat_pdl.cuh"
@@ -1435,27 +1434,40 @@ bool build_sched(const SchedSpec &sp, int npairs, TileSched &out) {
         out = cached;
         return true;
     }
-    std::vector<std::vector<uint16_t>> lists(static_cast<size_t>(npairs));
+    // no allocation here: a C entry point is above, which lets no exception escape
     using Load = std::pair<int64_t, int>;  // (load, pair): the smallest on top
-    std::priority_queue<Load, std::vector<Load>, std::greater<Load>> heap;
-    for (int q = 0; q < npairs; ++q) heap.push({0, q});
+    Load heap[kSchedPairs];
+    static uint16_t dealt[kSchedTiles];  // the tiles as dealt, and to whom (under the lock)
+    static uint8_t owner[kSchedTiles];
+    static_assert(kSchedPairs <= 256, "a pair's number is a byte");
+    for (int q = 0; q < npairs; ++q) heap[q] = {0, q};  // ascending: a heap already
     const bool first1 = sp.cost1 > sp.cost0;
+    int pos = 0;
     for (int k = 0; k < 2; ++k) {
         const int prob = (k == 0) == first1 ? 1 : 0;
         const int n = prob ? sp.tiles1 : sp.tiles0, base = prob ? sp.tiles0 : 0, cost = prob ? sp.cost1 : sp.cost0;
-        for (int i = 0; i < n; ++i) {
-            const Load top = heap.top();
-            heap.pop();
-            lists[static_cast<size_t>(top.second)].push_back(static_cast<uint16_t>(base + i));
-            heap.push({top.first + cost, top.second});
+        for (int i = 0; i < n; ++i, ++pos) {
+            std::pop_heap(heap, heap + npairs, std::greater<Load>());
+            Load &top = heap[npairs - 1];
+            dealt[pos] = static_cast<uint16_t>(base + i);
+            owner[pos] = static_cast<uint8_t>(top.second);
+            top.first += cost;
+            std::push_heap(heap, heap + npairs, std::greater<Load>());
         }
     }
-    int pos = 0;
-    for (int q = 0; q < npairs; ++q) {
+    // each pair's tiles side by side, in the order dealt
+    int next[kSchedPairs] = {};
+    for (int t = 0; t < total; ++t) ++next[owner[t]];
+    pos = 0;
+    for (int q = 0; q <= kSchedPairs; ++q) {
         out.begin[q] = static_cast<uint16_t>(pos);
-        for (uint16_t t : lists[static_cast<size_t>(q)]) out.tile[pos++] = t;
+        if (q < npairs) {
+            const int n = next[q];
+            next[q] = pos;
+            pos += n;
+        }
     }
-    for (int q = npairs; q <= kSchedPairs; ++q) out.begin[q] = static_cast<uint16_t>(pos);
+    for (int t = 0; t < total; ++t) out.tile[next[owner[t]]++] = dealt[t];
     last = sp;
     last_pairs = npairs;
     cached = out;
