@@ -49,3 +49,9 @@ def test_traffic_record_is_keyed_by_the_kernel_sources():
     # used only while the sources hash to the recorded value
     expected = rec["dram_bytes_per_launch"] if rec["kernel_source_hash"] == bench.kernel_source_hash() else None
     assert bench.load_traffic() == expected
+
+
+def test_traffic_record_is_of_the_current_sources():
+    """A change to the backward GEMM's sources takes the bench line's traffic away until the
+    capture (the record's own command) is taken again."""
+    assert bench.load_traffic() is not None
